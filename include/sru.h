@@ -356,9 +356,47 @@ sru_status sru_decode_step(const void* X_t, const void* W, const float* x_t, con
  * other B) the step runs the fused kernel above. */
 size_t sru_decode_workspace_bytes(int64_t B, int64_t d);
 
+/*
+ * Softmax cross entropy of a language model's last layer over its vocabulary
+ * (the page's models end in a linear map and a softmax), without storing the
+ * logits z = H W^T:
+ *   lse[i]  = log sum_v exp z[i][v]
+ *   loss[i] = lse[i] - z[i][targets[i]],  0 where targets[i] < 0 (not counted)
+ *   H (M, K) bf16   rows of the last layer's output
+ *   W (V, K) bf16   output matrix, one row per class
+ *   targets (M) int64;  loss, lse (M) fp32
+ * A target >= V is reported as SRU_ERR_INVALID by the next sru_sync_status();
+ * its row counts like one with a negative target.
+ * workspace: >= sru_softmax_loss_workspace_bytes(M, V, K, 0) bytes.
+ * Limits: K % 8 == 0; any M >= 0 and V >= 1 below 2^31.  Every pointer is
+ * 16-byte aligned.  fp32 accumulation throughout.
+ */
+size_t sru_softmax_loss_workspace_bytes(int64_t M, int64_t V, int64_t K, int backward);
+sru_status sru_softmax_loss(const void* H, const void* W, const int64_t* targets, float* loss, float* lse, int64_t M,
+                            int64_t V, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Backward of sru_softmax_loss for Loss = sum(dloss * loss):
+ *   dz[i][v] = dloss[i] (exp(z[i][v] - lse[i]) - [v = targets[i]]), 0 where targets[i] < 0
+ *   dH (M, K) = dz W,   dW (V, K) = dz^T H
+ * each of type F32 or BF16 (dh_t, dw_t), written; either may be NULL (not
+ * computed).  H, W, targets as given to the forward, lse as it wrote it.
+ * The logits are recomputed one piece of the vocabulary at a time; dz of a
+ * piece is rounded to bf16 (it is a tensor-core operand), the sums over the
+ * vocabulary and over the rows are fp32 and taken in a fixed order (the same
+ * bits every run).  M = 0 writes dW = 0.
+ * workspace: >= sru_softmax_loss_workspace_bytes(M, V, K, 1) bytes (which also
+ * serves the forward).  Limits as for the forward.
+ */
+sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t* targets, const float* lse,
+                                     const float* dloss, void* dH, int dh_t, void* dW, int dw_t, int64_t M, int64_t V,
+                                     int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, then read and clear the device error word of the
  * current device: SRU_ERR_TIMEOUT if a bounded wait expired since the last
- * call, SRU_ERR_CUDA if the stream reported an error, else SRU_OK. */
+ * call, SRU_ERR_INVALID if a kernel met an index out of range in its data (it
+ * skips such an entry), SRU_ERR_CUDA if the stream reported an error, else
+ * SRU_OK. */
 sru_status sru_sync_status(void* stream);
 
 #ifdef __cplusplus

@@ -13,6 +13,7 @@ element-wise recurrence), with a highway scale alpha.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -36,7 +37,8 @@ EXPORTED = ("sru_status_string", "sru_get_last_cuda_error", "sru_version", "sru_
             "sru_project_factored", "sru_project_factored_backward", "sru_project_factored_backward_workspace_bytes",
             "sru_attention_workspace_bytes",
             "sru_attention_project", "sru_attention_backward_workspace_bytes", "sru_attention_project_backward",
-            "sru_decode_workspace_bytes", "sru_decode_step", "sru_sync_status")
+            "sru_decode_workspace_bytes", "sru_decode_step",
+            "sru_softmax_loss_workspace_bytes", "sru_softmax_loss", "sru_softmax_loss_backward", "sru_sync_status")
 
 
 class SRUError(RuntimeError):
@@ -109,6 +111,13 @@ def load_library(path: str = LIB_PATH):
     lib.sru_decode_step.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _f32, _vp, ctypes.c_size_t, _vp]
     lib.sru_decode_workspace_bytes.restype = ctypes.c_size_t
     lib.sru_decode_workspace_bytes.argtypes = [_i64, _i64]
+    lib.sru_softmax_loss_workspace_bytes.restype = ctypes.c_size_t
+    lib.sru_softmax_loss_workspace_bytes.argtypes = [_i64, _i64, _i64, _int]
+    lib.sru_softmax_loss.restype = _int
+    lib.sru_softmax_loss.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, ctypes.c_size_t, _vp]
+    lib.sru_softmax_loss_backward.restype = _int
+    lib.sru_softmax_loss_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _int, _i64, _i64, _i64,
+                                              _vp, ctypes.c_size_t, _vp]
     lib.sru_sync_status.restype = _int
     lib.sru_sync_status.argtypes = [_vp]
     _lib = lib
@@ -365,6 +374,76 @@ def sru_decode_step(X_t, W, x_t, v, b, c, h_t, alpha: float = 1.0, workspace=Non
                                _stream(stream)),
            "sru_decode_step")
     return h_t, c
+
+
+def _same_device(*tensors):
+    """Context that makes the tensors' device current for a launch; raises unless they share one CUDA device."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1 or next(iter(devices)).type != "cuda":
+        raise ValueError("tensors must live on one CUDA device")
+    index = next(iter(devices)).index
+    return contextlib.nullcontext() if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
+def _scratch(nbytes: int, device, stream) -> Optional[torch.Tensor]:
+    """A workspace for one call: torch reuses it only after the call's stream has passed it."""
+    if nbytes == 0:
+        return None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None and stream != torch.cuda.current_stream(device):
+        ws.record_stream(stream)
+    return ws
+
+
+def sru_softmax_loss_workspace_bytes(M: int, V: int, K: int, backward: bool = True) -> int:
+    """Workspace of sru_softmax_loss and, with backward, of sru_softmax_loss_backward (one buffer serves both)."""
+    return int(load_library().sru_softmax_loss_workspace_bytes(M, V, K, int(bool(backward))))
+
+
+def _loss_shapes(H, W, targets, *rows):
+    M, K = H.shape
+    V = W.shape[0]
+    if tuple(W.shape) != (V, K) or tuple(targets.shape) != (M,) or any(tuple(t.shape) != (M,) for t in rows):
+        raise ValueError("shape mismatch")
+    return M, V, K
+
+
+def sru_softmax_loss(H, W, targets, loss, lse, workspace=None, stream=None):
+    """Softmax cross entropy of every row over the vocabulary, logits z = H W^T never
+    stored: lse = logsumexp(z), loss = lse - z[target] (0 where target < 0).
+    H (M, K) and W (V, K) bf16, targets (M,) int64; loss and lse (M,) fp32 written
+    in place.  A workspace of sru_softmax_loss_workspace_bytes(M, V, K, False)
+    bytes is allocated when none is given."""
+    lib = load_library()
+    M, V, K = _loss_shapes(H, W, targets, loss, lse)
+    with _same_device(H, W, targets, loss, lse, workspace):
+        if workspace is None:
+            workspace = _scratch(sru_softmax_loss_workspace_bytes(M, V, K, False), H.device, stream)
+        _check(lib.sru_softmax_loss(_ptr(H, torch.bfloat16), _ptr(W, torch.bfloat16), _ptr(targets, torch.int64),
+                                    _ptr(loss, torch.float32), _ptr(lse, torch.float32), M, V, K, _ptr(workspace),
+                                    _nbytes(workspace), _stream(stream)), "sru_softmax_loss")
+    return loss, lse
+
+
+def sru_softmax_loss_backward(H, W, targets, lse, dloss, dH=None, dW=None, workspace=None, stream=None):
+    """Gradients of sum(dloss * loss): dz = dloss (softmax(z) - onehot(target)) (0 where
+    target < 0), dH = dz W (M, K), dW = dz^T H (V, K), each fp32 or bf16, written in
+    place; either may be None.  lse as sru_softmax_loss wrote it, dloss (M,) fp32.
+    A workspace of sru_softmax_loss_workspace_bytes(M, V, K) bytes is allocated when
+    none is given."""
+    lib = load_library()
+    M, V, K = _loss_shapes(H, W, targets, lse, dloss)
+    if (dH is not None and tuple(dH.shape) != (M, K)) or (dW is not None and tuple(dW.shape) != (V, K)):
+        raise ValueError("gradient shape mismatch")
+    with _same_device(H, W, targets, lse, dloss, dH, dW, workspace):
+        if workspace is None:
+            workspace = _scratch(sru_softmax_loss_workspace_bytes(M, V, K, True), H.device, stream)
+        _check(lib.sru_softmax_loss_backward(
+            _ptr(H, torch.bfloat16), _ptr(W, torch.bfloat16), _ptr(targets, torch.int64), _ptr(lse, torch.float32),
+            _ptr(dloss, torch.float32), _ptr(dH), SRU_F32 if dH is None else _dtype_code(dH), _ptr(dW),
+            SRU_F32 if dW is None else _dtype_code(dW), M, V, K, _ptr(workspace), _nbytes(workspace),
+            _stream(stream)), "sru_softmax_loss_backward")
+    return dH, dW
 
 
 def sru_sync_status(stream=None) -> int:

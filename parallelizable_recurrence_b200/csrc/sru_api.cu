@@ -18,6 +18,7 @@
 #include "sru_decode.cuh"
 #include "sru_scan.cuh"
 #include "sru_fused.cuh"
+#include "sru_loss.cuh"
 
 namespace {
 
@@ -1719,6 +1720,222 @@ sru_status sru_decode_step(const void* X_t, const void* W, const float* x_t, con
     }
 }
 
+}  // extern "C"
+
+// ---- softmax cross entropy over the vocabulary
+// dz of one piece of the vocabulary (M x Vc bf16) stays within this budget.  The
+// gradients read each piece twice; a smaller piece costs one more read and write
+// of the M x K fp32 sum dH, a larger one memory.
+constexpr size_t kLossPieceBytes = (size_t)512 << 20;
+struct LossPlan {
+    int64_t n_tiles, Vc, pieces;
+    SplitPlan dh, dw;
+    size_t partial_off, target_off, dz_off, dh_off, dw_off, forward_total, total;
+};
+static LossPlan loss_plan(int64_t M, int64_t V, int64_t K, bool backward) {
+    LossPlan p{};
+    p.n_tiles = (V + sru::gemm::P_BN - 1) / sru::gemm::P_BN;
+    p.target_off = round256((size_t)p.n_tiles * M * sizeof(float2));
+    p.forward_total = p.target_off + round256((size_t)M * 4);
+    p.total = p.forward_total;
+    if (!backward) return p;
+    // equal pieces, whole tiles (a piece starts on a 16-byte boundary of dz and W)
+    const int64_t most = std::max<int64_t>(kLossPieceBytes / ((size_t)M * 2) / sru::gemm::P_BN, 4) * sru::gemm::P_BN;
+    const int64_t n = (V + most - 1) / most;
+    p.Vc = ((V + n - 1) / n + sru::gemm::P_BN - 1) / sru::gemm::P_BN * sru::gemm::P_BN;
+    p.pieces = (V + p.Vc - 1) / p.Vc;
+    p.dh = split_plan(M, K, std::min(p.Vc, V));
+    p.dw = split_plan(std::min(p.Vc, V), K, M);
+    p.dh_off = round256((size_t)M * p.Vc * 2);
+    p.dw_off = p.dh_off + round256(p.dh.splits > 1 ? p.dh.bytes : (p.pieces > 1 ? (size_t)M * K * 4 : 0));
+    p.total = std::max(p.forward_total, p.dw_off + round256(p.dw.bytes));
+    return p;
+}
+static sru_status check_loss_sizes(int64_t M, int64_t V, int64_t K) {
+    if (M < 0 || V < 1 || K < 1) return SRU_ERR_INVALID;
+    if (K % 8 != 0) return SRU_ERR_UNSUPPORTED;
+    const int64_t lim = (int64_t)1 << 31;
+    if (M >= lim || V >= lim || K >= lim) return SRU_ERR_UNSUPPORTED;
+    if (((M + 255) / 256) * ((V + 255) / 256) >= lim || ((V + 255) / 256) * ((K + 255) / 256) >= lim ||
+        ((M + 255) / 256) * ((K + 255) / 256) >= lim)
+        return SRU_ERR_UNSUPPORTED;
+    return SRU_OK;
+}
+template <int EPI>
+static sru_status launch_vocab(const CUtensorMap& mh, const CUtensorMap& mw, const CUtensorMap& mdz,
+                               const sru::loss::LossArgs& a, int64_t M, int64_t N, int64_t K, cudaStream_t st) {
+    auto kern = sru::loss::vocab_gemm_kernel<EPI>;
+    SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kern), sru::gemm::P_SMEM_BYTES));
+    const int64_t units = ((M + sru::gemm::P_BM - 1) / sru::gemm::P_BM) * ((N + sru::gemm::P_BN - 1) / sru::gemm::P_BN);
+    const int64_t pairs = std::min<int64_t>(units, sm_count() / 2);
+    kern<<<(unsigned)(2 * pairs), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st>>>(mh, mw, mdz, a, (int)M, (int)N,
+                                                                                     (int)K);
+    SRU_CUDA_TRY(cudaGetLastError());
+    return SRU_OK;
+}
+template <bool A_MN, bool B_MN, int OUT>
+static sru_status launch_slabs(const CUtensorMap& ma, const CUtensorMap& mb, void* slabs, int64_t R, int64_t C,
+                               int64_t Kr, int64_t splits, int64_t slab_rows, int64_t all_splits, cudaStream_t st) {
+    auto kern = sru::gemm::tc_gemm_pair_kernel<A_MN, B_MN, OUT>;
+    SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kern), sru::gemm::P_SMEM_BYTES));
+    CUtensorMap mo;
+    const uint64_t dims[2] = {(uint64_t)C, (uint64_t)(slab_rows * all_splits)};
+    const uint64_t strides[1] = {(uint64_t)C * 4};
+    const uint32_t box[2] = {(uint32_t)sru::gemm::EpiChunk<OUT>::kCols, 32};
+    if (!make_map(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, slabs, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+        return SRU_ERR_INVALID;
+    const int64_t units =
+        ((R + sru::gemm::P_BM - 1) / sru::gemm::P_BM) * ((C + sru::gemm::P_BN - 1) / sru::gemm::P_BN) * splits;
+    const int64_t pairs = std::min<int64_t>(units, sm_count() / 2);
+    kern<<<(unsigned)(2 * pairs), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st>>>(
+        ma, mb, mo, (int)R, (int)C, (int)Kr, (int)splits, 1, 0, (int)slab_rows);
+    SRU_CUDA_TRY(cudaGetLastError());
+    return SRU_OK;
+}
+static sru_status sum_slabs(const void* slabs, void* out, int out_t, int64_t R, int64_t C, int64_t slab_rows,
+                            int64_t splits, cudaStream_t st) {
+    const size_t n4 = (size_t)R * C / 4;
+    const unsigned grid = (unsigned)std::min<size_t>(blocks_for(n4, 256), (size_t)sm_count() * 8);
+    const float4* s = static_cast<const float4*>(slabs);
+    if (out_t == SRU_BF16)
+        sru::loss::slab_sum_kernel<<<grid, 256, 0, st>>>(s, static_cast<__nv_bfloat16*>(out), (int)R, (int)(C / 4),
+                                                         (long long)slab_rows, (int)splits);
+    else
+        sru::loss::slab_sum_kernel<<<grid, 256, 0, st>>>(s, static_cast<float*>(out), (int)R, (int)(C / 4),
+                                                         (long long)slab_rows, (int)splits);
+    SRU_CUDA_TRY(cudaGetLastError());
+    return SRU_OK;
+}
+static sru_status zero_typed(void* p, int t, size_t n, cudaStream_t st) {
+    SRU_CUDA_TRY(cudaMemsetAsync(p, 0, n * (t == SRU_BF16 ? 2 : 4), st));
+    return SRU_OK;
+}
+
+extern "C" {
+
+size_t sru_softmax_loss_workspace_bytes(int64_t M, int64_t V, int64_t K, int backward) {
+    if (check_loss_sizes(M, V, K) != SRU_OK || M == 0) return 0;
+    return loss_plan(M, V, K, backward != 0).total;
+}
+
+sru_status sru_softmax_loss(const void* H, const void* W, const int64_t* targets, float* loss, float* lse, int64_t M,
+                            int64_t V, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+    sru_status s = check_loss_sizes(M, V, K);
+    if (s != SRU_OK || M == 0) return s;
+    if (!H || !W || !targets || !loss || !lse || !workspace) return SRU_ERR_INVALID;
+    if (!aligned16(H) || !aligned16(W) || !aligned16(targets) || !aligned16(loss) || !aligned16(lse) ||
+        !aligned16(workspace))
+        return SRU_ERR_INVALID;
+    const LossPlan p = loss_plan(M, V, K, false);
+    if (workspace_bytes < p.total) return SRU_ERR_INVALID;
+    cudaStream_t st = as_stream(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    CUtensorMap mh, mw;
+    if (!map_kmajor(&mh, H, M, K, sru::gemm::P_CM) || !map_kmajor(&mw, W, V, K, kGemmBRows)) return SRU_ERR_INVALID;
+    sru::loss::LossArgs a{};
+    a.targets = reinterpret_cast<const long long*>(targets);
+    a.partial = reinterpret_cast<float2*>(ws + p.partial_off);
+    a.target_logit = reinterpret_cast<float*>(ws + p.target_off);
+    a.V = V;
+    s = launch_vocab<sru::loss::kStats>(mh, mw, mh, a, M, V, K, st);
+    if (s != SRU_OK) return s;
+    sru::loss::vocab_loss_kernel<<<blocks_for((size_t)M, sru::loss::kJoinRows),
+                                   sru::loss::kJoinRows * sru::loss::kJoinGroups, 0, st>>>(
+        a.partial, a.target_logit, a.targets, loss, lse, (int)M, (int)p.n_tiles, (long long)V);
+    SRU_CUDA_TRY(cudaGetLastError());
+    return SRU_OK;
+}
+
+sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t* targets, const float* lse,
+                                     const float* dloss, void* dH, int dh_t, void* dW, int dw_t, int64_t M, int64_t V,
+                                     int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+    sru_status s = check_loss_sizes(M, V, K);
+    if (s != SRU_OK) return s;
+    if ((dH && dh_t != SRU_F32 && dh_t != SRU_BF16) || (dW && dw_t != SRU_F32 && dw_t != SRU_BF16))
+        return SRU_ERR_INVALID;
+    if (!aligned16(dH) || !aligned16(dW)) return SRU_ERR_INVALID;  // null: that gradient is not computed
+    cudaStream_t st = as_stream(stream);
+    if (M == 0) return dW ? zero_typed(dW, dw_t, (size_t)V * K, st) : SRU_OK;
+    if (!dH && !dW) return SRU_OK;
+    if (!H || !W || !targets || !lse || !dloss || !workspace) return SRU_ERR_INVALID;
+    if (!aligned16(H) || !aligned16(W) || !aligned16(targets) || !aligned16(lse) || !aligned16(dloss) ||
+        !aligned16(workspace))
+        return SRU_ERR_INVALID;
+    const LossPlan p = loss_plan(M, V, K, true);
+    if (workspace_bytes < p.total) return SRU_ERR_INVALID;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    void* dz = ws + p.dz_off;
+    void* slab_h = ws + p.dh_off;
+    void* slab_w = ws + p.dw_off;
+    CUtensorMap mh, mw, mdz, ma, mb;
+    if (!map_kmajor(&mh, H, M, K, sru::gemm::P_CM)) return SRU_ERR_INVALID;
+    sru::loss::LossArgs a{};
+    a.targets = reinterpret_cast<const long long*>(targets);
+    a.lse = lse;
+    a.dloss = dloss;
+    a.V = V;
+    // dH is summed over the pieces in fp32: in place, or in the workspace when it is split
+    // along the vocabulary or leaves as bf16
+    const bool h_in_slabs = p.dh.splits > 1 || (p.pieces > 1 && dh_t == SRU_BF16);
+    using sru::gemm::kOutBF16;
+    using sru::gemm::kOutF32;
+    using sru::gemm::kOutF32Acc;
+    for (int64_t v0 = 0; v0 < V; v0 += p.Vc) {
+        const int64_t n = std::min(p.Vc, V - v0);
+        const __nv_bfloat16* Wp = static_cast<const __nv_bfloat16*>(W) + (size_t)v0 * K;
+        {
+            const uint64_t dims[2] = {(uint64_t)n, (uint64_t)M};
+            const uint64_t strides[1] = {(uint64_t)p.Vc * 2};
+            const uint32_t box[2] = {(uint32_t)sru::gemm::EpiChunk<kOutBF16>::kCols, 32};
+            if (!map_kmajor(&mw, Wp, n, K, kGemmBRows) ||
+                !make_map(&mdz, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dz, dims, strides, box,
+                          CU_TENSOR_MAP_SWIZZLE_128B))
+                return SRU_ERR_INVALID;
+        }
+        a.v0 = v0;
+        s = launch_vocab<sru::loss::kGrad>(mh, mw, mdz, a, M, n, K, st);
+        if (s != SRU_OK) return s;
+        if (dH) {
+            // dH += dz W: A = dz (M x n) K-major, B(c = k, red = v) = W[v][k] MN-major
+            if (!map_kmajor(&ma, dz, M, n, sru::gemm::P_CM, p.Vc) || !map_mnmajor(&mb, Wp, K, n, K))
+                return SRU_ERR_INVALID;
+            if (p.dh.splits > 1) {
+                // no empty part in a shorter last piece either (see split_plan)
+                const int64_t kb = (n + sru::gemm::BK - 1) / sru::gemm::BK;
+                const int64_t per = (kb + p.dh.splits - 1) / p.dh.splits, S = (kb + per - 1) / per;
+                s = v0 == 0 ? launch_slabs<false, true, kOutF32>(ma, mb, slab_h, M, K, n, S, p.dh.slab_rows,
+                                                                 p.dh.splits, st)
+                            : launch_slabs<false, true, kOutF32Acc>(ma, mb, slab_h, M, K, n, S, p.dh.slab_rows,
+                                                                    p.dh.splits, st);
+            } else {
+                void* out = h_in_slabs ? slab_h : dH;
+                if (v0 != 0) s = launch_tc_gemm<false, true, kOutF32Acc>(ma, mb, out, M, K, n, st);
+                else if (!h_in_slabs && dh_t == SRU_BF16)
+                    s = launch_tc_gemm<false, true, kOutBF16>(ma, mb, out, M, K, n, st);
+                else s = launch_tc_gemm<false, true, kOutF32>(ma, mb, out, M, K, n, st, 1, -1, /*tail_split=*/true);
+            }
+            if (s != SRU_OK) return s;
+        }
+        if (dW) {
+            // this piece's rows of dW = dz^T H: A = dz read as (n x M) MN-major, B(c = k, red = m) = H[m][k]
+            if (!map_mnmajor(&ma, dz, n, M, p.Vc) || !map_mnmajor(&mb, H, K, M, K)) return SRU_ERR_INVALID;
+            void* out = static_cast<uint8_t*>(dW) + (size_t)v0 * K * (dw_t == SRU_BF16 ? 2 : 4);
+            if (p.dw.splits > 1) {
+                s = launch_slabs<true, true, kOutF32>(ma, mb, slab_w, n, K, M, p.dw.splits, p.dw.slab_rows,
+                                                      p.dw.splits, st);
+                if (s == SRU_OK) s = sum_slabs(slab_w, out, dw_t, n, K, p.dw.slab_rows, p.dw.splits, st);
+            } else if (dw_t == SRU_BF16) {
+                s = launch_tc_gemm<true, true, kOutBF16>(ma, mb, out, n, K, M, st);
+            } else {
+                s = launch_tc_gemm<true, true, kOutF32>(ma, mb, out, n, K, M, st, 1, -1, /*tail_split=*/true);
+            }
+            if (s != SRU_OK) return s;
+        }
+    }
+    if (dH && h_in_slabs) return sum_slabs(slab_h, dH, dh_t, M, K, p.dh.slab_rows, p.dh.splits, st);
+    return SRU_OK;
+}
+
 sru_status sru_sync_status(void* stream) {
     cudaError_t e = cudaStreamSynchronize(as_stream(stream));
     if (e != cudaSuccess) return cuda_fail(e);
@@ -1729,7 +1946,7 @@ sru_status sru_sync_status(void* stream) {
         const unsigned zero = 0;
         e = cudaMemcpyToSymbol(sru::g_error_word, &zero, sizeof(zero));
         if (e != cudaSuccess) return cuda_fail(e);
-        return SRU_ERR_TIMEOUT;
+        return word == sru::kErrBadIndex ? SRU_ERR_INVALID : SRU_ERR_TIMEOUT;
     }
     return SRU_OK;
 }

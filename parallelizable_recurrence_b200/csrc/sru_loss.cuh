@@ -1,0 +1,362 @@
+// sru_loss.cuh -- softmax cross entropy over a large vocabulary, with its
+// gradients, without keeping the logits.
+//
+// For a row h_i of the last layer's output and the output matrix W (V, K):
+//   z_i = W h_i,   lse_i = log sum_v exp z_iv,   loss_i = lse_i - z_i,t(i)
+//   dz_iv = g_i (exp(z_iv - lse_i) - [v = t(i)]),   dH = dz W,   dW = dz^T H
+// vocab_gemm_kernel runs z = H W^T as the pair GEMM of sru_gemm.cuh does (a
+// cluster of two CTAs per 256 x 256 tile, TMA-fed ring, tcgen05.mma
+// cta_group::2, two accumulators) and never stores z: a TMEM lane holds 256
+// logits of one row, so each epilogue thread reduces its row alone, without
+// shuffles.  Two epilogues:
+//   kStats  running maximum and sum of exponentials of the row's 256 logits
+//           (8 bytes per row and tile; vocab_loss_kernel joins the tiles) and,
+//           in the one tile that holds it, the target's logit;
+//   kGrad   dz of the tile from the row's lse and weight g, rounded to bf16 as
+//           the operand of the two gradient products, stored by TMA.
+// The gradients run over pieces of the vocabulary, so that dz never takes more
+// than a bounded buffer; z is recomputed there (2 M V K operations on top of
+// the gradients' 4 M V K), since reading it back in fp32 and writing it costs
+// more than the product for K up to about 2000.
+#pragma once
+
+#include "sru_gemm.cuh"
+
+namespace sru {
+namespace loss {
+
+using namespace gemm;
+
+enum Epilogue : int { kStats = 0, kGrad = 1 };
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Tiles in groups of kGroupM row tiles, the row tile fastest: the 74 pairs of a
+// round then cover about 8 x 9 tiles, and a piece of W is read from memory once
+// per group of 2048 rows instead of once per 256.
+constexpr int kGroupM = 8;
+__device__ __forceinline__ void unit_tile(int u, int m_tiles, int n_tiles, int& tm, int& tn) {
+    const int per = kGroupM * n_tiles, g = u / per, r = u - g * per;
+    const int gm = min(kGroupM, m_tiles - g * kGroupM);
+    tn = r / gm;
+    tm = g * kGroupM + r - tn * gm;
+}
+
+struct LossArgs {
+    const long long* targets;  // (M): the class of each row; negative = not counted
+    float2* partial;           // kStats: (n_tiles, M) maximum and sum of exponentials
+    float* target_logit;       // kStats: (M)
+    const float* lse;          // kGrad: (M)
+    const float* dloss;        // kGrad: (M)
+    long long v0, V;           // first column of this piece of the vocabulary, its whole size
+};
+
+// M rows, N columns of this piece, K the reduction.  map_w starts at row v0 of W.
+template <int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    vocab_gemm_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_w,
+                      const __grid_constant__ CUtensorMap map_dz, LossArgs a, int M, int N, int K) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* epi = smem + P_STAGES * P_STAGE_BYTES;
+    uint64_t* full = reinterpret_cast<uint64_t*>(epi + P_EPI_BYTES);
+    uint64_t* empty = full + P_STAGES;
+    uint64_t* tfull = empty + P_STAGES;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile uint32_t* consumed = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair_id = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+    const int m_tiles = (M + P_BM - 1) / P_BM, n_tiles = (N + P_BN - 1) / P_BN;
+    const int kblocks = (K + BK - 1) / BK;
+    const int units = m_tiles * n_tiles;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < P_STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 8);  // 4 epilogue warps of each CTA
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        *consumed = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&map_h);
+        tma_prefetch_desc(&map_w);
+        if (EPI == kGrad) tma_prefetch_desc(&map_dz);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, P_TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before_sync();
+    cluster_sync_all();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t leader_full0 = mapa_shared(smem_u32(&full[0]), 0);
+    const uint32_t leader_tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------------ producer (both CTAs)
+            uint32_t issued = 0, phase = 0;
+            int stage = 0;
+            for (int u = pair_id; u < units && !*abort_flag; u += n_pairs) {
+                int tm, tn;
+                unit_tile(u, m_tiles, n_tiles, tm, tn);
+                const int m0 = tm * P_BM + (int)rank * P_CM, n0 = tn * P_BN + (int)rank * P_CN;
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1u, kErrTimeoutMma) || *abort_flag) {
+                        *abort_flag = 1;
+                        break;
+                    }
+                    uint8_t* a_dst = smem + stage * P_STAGE_BYTES;
+                    const uint32_t bar = leader_full0 + (uint32_t)stage * 8u;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * P_STAGE_BYTES);
+                    tma_load_2d_pair(a_dst, &map_h, bar, kb * BK, m0);
+                    tma_load_2d_pair(a_dst + P_A_BYTES, &map_w, bar, kb * BK, n0);
+                    ++issued;
+                    if (++stage == P_STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (*abort_flag && rank == 0) {
+                for (uint32_t q = *consumed; q < issued; ++q)
+                    mbar_wait(&full[q % P_STAGES], (q / P_STAGES) & 1u, kErrTimeoutLoad);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ------------------------------------------------------ MMA issuer (leader)
+            constexpr uint32_t idesc = idesc_bf16_pair(false, false);
+            int stage = 0, it = 0;
+            uint32_t phase = 0, nconsumed = 0;
+            for (int u = pair_id; u < units && !*abort_flag; u += n_pairs, ++it) {
+                const int acc = it & 1;
+                if (!mbar_wait(&tempty[acc], ((it >> 1) & 1) ^ 1u, kErrTimeoutEpilogue)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + acc * P_BN;
+                bool ok = true;
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!mbar_wait(&full[stage], phase, kErrTimeoutLoad)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t a_addr = smem_u32(smem + stage * P_STAGE_BYTES), b_addr = a_addr + P_A_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk)
+                        tc_mma_bf16_pair(d_tmem, smem_desc_sw128(a_addr + kk * 32, 16, 1024),
+                                         smem_desc_sw128(b_addr + kk * 32, 16, 1024), idesc,
+                                         (kb != 0 || kk != 0) ? 1u : 0u);
+                    tc_commit_pair_mc(&empty[stage], 0x3);
+                    *consumed = ++nconsumed;
+                    if (++stage == P_STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                tc_commit_pair_mc(&tfull[acc], 0x3);
+            }
+            tc_commit_pair_mc(drain, 0x1);
+            mbar_wait(drain, 0, kErrTimeoutMma);
+        }
+    } else {
+        // ---------------------------------------------------------- epilogue (both CTAs)
+        const int quarter = warp & 3;
+        int it = 0;
+        uint32_t nstaged = 0;
+        for (int u = pair_id; u < units; u += n_pairs, ++it) {
+            int tm, tn;
+            unit_tile(u, m_tiles, n_tiles, tm, tn);
+            const int acc = it & 1;
+            const int m0 = tm * P_BM + (int)rank * P_CM, n0 = tn * P_BN;
+            const int row = m0 + quarter * 32 + lane;
+            const bool live = row < M;
+            // the row's operands, fetched while the product runs
+            long long tgt = live ? a.targets[row] : -1;
+            if (tgt >= a.V) tgt = -1;  // not a class: vocab_loss_kernel reports it
+            const long long trel = tgt < 0 ? -1 : tgt - a.v0 - n0;  // target's column in this tile, if inside
+            float lse2 = 0.f, g = 0.f;
+            if (EPI == kGrad && tgt >= 0) {
+                lse2 = a.lse[row] * kLog2e;
+                g = a.dloss[row];
+            }
+            const bool ok = mbar_wait(&tfull[acc], (it >> 1) & 1, kErrTimeoutMma);
+            if (!__all_sync(0xffffffffu, ok) || *abort_flag) {
+                *abort_flag = 1;
+                break;
+            }
+            tc_fence_after_sync();
+            constexpr int NC = 64, NG = P_BN / NC;
+            const int ncol = min(P_BN, N - n0);
+            const int ng = (ncol + NC - 1) / NC;
+            const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * P_BN;
+            float top = -INFINITY, sum = 0.f;
+            uint32_t r0[NC], r1[NC];
+            tmem_ld_cols<NC>(tacc, r0);
+#pragma unroll
+            for (int c = 0; c < NG; ++c) {
+                if (c >= ng) break;  // uniform across the warp
+                uint32_t(&cur)[NC] = (c & 1) ? r1 : r0;
+                uint32_t(&nxt)[NC] = (c & 1) ? r0 : r1;
+                tc_wait_ld();
+                if (c + 1 < ng) tmem_ld_cols<NC>(tacc + (c + 1) * NC, nxt);
+                const long long tc = trel - c * NC;
+                const bool has_target = tc >= 0 && tc < NC;
+                if (EPI == kStats) {
+                    if (ncol < (c + 1) * NC) {
+                        // columns behind the vocabulary hold products with zero rows
+#pragma unroll
+                        for (int e = 0; e < NC; ++e)
+                            if (c * NC + e >= ncol) cur[e] = 0xff800000u;
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = 0; e < NC; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(cur[e]));
+                    const float nt = fmaxf(top, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    const float base = (nt == -INFINITY ? 0.f : nt) * kLog2e;
+                    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int e = 0; e < NC; ++e)
+                        s[e & 3] += ex2_approx(__fmaf_rn(__uint_as_float(cur[e]), kLog2e, -base));
+                    sum = __fmaf_rn(sum, ex2_approx(__fmaf_rn(top, kLog2e, -base)), (s[0] + s[1]) + (s[2] + s[3]));
+                    top = nt;
+                    if (has_target) {
+                        float zt = 0.f;
+#pragma unroll
+                        for (int e = 0; e < NC; ++e)
+                            if (e == (int)tc) zt = __uint_as_float(cur[e]);
+                        a.target_logit[row] = zt;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < NC; ++e) {
+                        const float p = ex2_approx(__fmaf_rn(__uint_as_float(cur[e]), kLog2e, -lse2)) * g;
+                        cur[e] = g == 0.f ? 0u : __float_as_uint(p);  // rows not counted: exactly 0
+                    }
+                    float pt = 0.f;
+                    if (has_target) {
+#pragma unroll
+                        for (int e = 0; e < NC; ++e)
+                            if (e == (int)tc) pt = __uint_as_float(cur[e]);
+                    }
+                    const uint32_t buf = smem_u32(epi) + (uint32_t)(quarter * 2 + (nstaged & 1)) * P_EPI_BUF;
+                    if (nstaged >= 2) {
+                        if (lane == 0) bulk_wait_group_read<1>();
+                        __syncwarp();
+                    }
+                    epilogue_stage_row<kOutBF16>(buf, lane, cur);
+                    if (has_target) {
+                        // (element tc of row `lane` in the staging buffer's swizzle)
+                        const uint32_t off = lane * 128u + ((((uint32_t)tc >> 3) ^ (lane & 7u)) << 4) + (tc & 7) * 2u;
+                        *reinterpret_cast<__nv_bfloat16*>(epi + (size_t)(quarter * 2 + (nstaged & 1)) * P_EPI_BUF +
+                                                          off) = __float2bfloat16_rn(pt - g);
+                    }
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&map_dz, epi + (size_t)(quarter * 2 + (nstaged & 1)) * P_EPI_BUF, n0 + c * NC,
+                                     m0 + quarter * 32);
+                        bulk_commit_group();
+                    }
+                    ++nstaged;
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(leader_tempty0 + (uint32_t)acc * 8u);
+            if (EPI == kStats && live) a.partial[(size_t)tn * M + row] = make_float2(top, sum);
+        }
+        if (EPI == kGrad && lane == 0) bulk_wait_group<0>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem_base, P_TMEM_COLS);
+    }
+}
+
+// Joins a row's tiles: lse = m + log sum_t s_t exp(m_t - m) with m the largest
+// m_t; loss = lse - z_target, 0 for rows that are not counted.  32 rows x 32
+// tile groups per CTA (consecutive threads read consecutive rows).
+constexpr int kJoinRows = 32, kJoinGroups = 32;
+__global__ void __launch_bounds__(kJoinRows* kJoinGroups)
+    vocab_loss_kernel(const float2* __restrict__ partial, const float* __restrict__ target_logit,
+                      const long long* __restrict__ targets, float* __restrict__ loss, float* __restrict__ lse,
+                      int M, int n_tiles, long long V) {
+    __shared__ float2 part[kJoinGroups][kJoinRows + 1];
+    const int r = threadIdx.x % kJoinRows, q = threadIdx.x / kJoinRows;
+    const int row = blockIdx.x * kJoinRows + r;
+    float top = -INFINITY, sum = 0.f;
+    auto join = [&](float2 b) {
+        const float nt = fmaxf(top, b.x);
+        const float base = nt == -INFINITY ? 0.f : nt;
+        sum = sum * __expf(top - base) + b.y * __expf(b.x - base);
+        top = nt;
+    };
+    if (row < M) {
+#pragma unroll 4
+        for (int t = q; t < n_tiles; t += kJoinGroups) join(partial[(size_t)t * M + row]);
+    }
+    part[q][r] = make_float2(top, sum);
+    __syncthreads();
+    if (q != 0 || row >= M) return;
+    for (int i = 1; i < kJoinGroups; ++i) join(part[i][r]);
+    const float total = top + logf(sum);
+    const long long t = targets[row];
+    if (t >= V) record_error(kErrBadIndex);
+    lse[row] = total;
+    loss[row] = t >= 0 && t < V ? total - target_logit[row] : 0.f;
+}
+
+// out[r][c] = sum over s = 0, 1, .. of slabs[s * slab_rows + r][c] in that order,
+// four columns per thread (C % 4 == 0).
+template <typename OutT>
+__global__ void __launch_bounds__(256) slab_sum_kernel(const float4* __restrict__ slabs, OutT* __restrict__ out,
+                                                       int R, int C4, long long slab_rows, int splits) {
+    const size_t n = (size_t)R * C4;
+    for (size_t e = blockIdx.x * (size_t)256 + threadIdx.x; e < n; e += (size_t)gridDim.x * 256) {
+        float4 acc = slabs[e];
+        for (int sp = 1; sp < splits; ++sp) {
+            const float4 v = slabs[(size_t)sp * slab_rows * C4 + e];
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+        }
+        if (sizeof(OutT) == 4) {
+            reinterpret_cast<float4*>(out)[e] = acc;
+        } else {
+            __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+            reinterpret_cast<uint2*>(out)[e] =
+                make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+        }
+    }
+}
+
+}  // namespace loss
+}  // namespace sru

@@ -25,6 +25,7 @@ enum DeviceError : unsigned {
     kErrTimeoutMma = 2,       // a tensor-core stage did not complete in time
     kErrTimeoutEpilogue = 3,  // the accumulator was not released in time
     kErrTimeoutScan = 4,      // a scan predecessor never published its carry
+    kErrBadIndex = 5,         // an index in the call's data (a page, slot or target) is out of range
 };
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
