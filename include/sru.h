@@ -392,6 +392,85 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
                                      const float* dloss, void* dH, int dh_t, void* dW, int dw_t, int64_t M, int64_t V,
                                      int64_t K, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * The paged key/value cache of SRU++ decoding.  The page's models attend at
+ * inference to the tokens seen so far; their keys and values live in pages of
+ * page_size tokens that a request gets as it grows:
+ *   k_cache, v_cache (pages, Hkv, page_size, D) bf16
+ *   table (B, max_pages) int32: request b's token t is row t % page_size of page
+ *     table[b][t / page_size]; entries behind its last page are not read
+ *   slot of a token: table[b][t / page_size] * page_size + t % page_size
+ *   free_pages (pages) int32: a stack of the pages that no request holds,
+ *     *free_count of them
+ *
+ * sru_cache_extend: the bookkeeping of one serving step, from device-side
+ * lengths, without a host round trip.  Request b holds lengths[b] tokens and
+ * brings new_tokens[b] more; a negative new_tokens[b] releases it.
+ *   1. The pages of the released requests go onto the stack, in request order.
+ *   2. In request order, a request takes the pages that its new tokens need
+ *      beyond those it holds off the top of the stack, as long as the sum of the
+ *      needs up to and with it is within the stack's height; otherwise, or when
+ *      its tokens exceed max_pages * page_size, or when the step's tokens up to and
+ *      with its own exceed T, it is refused and keeps what it had (a need that
+ *      does not fit the stack still counts in the sum).
+ *   table, free_pages: updated in place.
+ *   lengths_out (B): lengths[b] + new_tokens[b]; lengths[b] when refused; 0 when
+ *     released.  May be lengths itself.
+ *   free_count_out (1): the stack's new height.  May be free_count itself.
+ *   offsets (B + 1): the first row of each request's tokens in the step (running
+ *     sum of the non-negative new_tokens, refused ones too; its total must stay
+ *     below 2^31), and their number.
+ *   slots (T): the slot of each row; -1 for the rows of refused requests and for
+ *     the rows behind the last token.
+ *   refused (1, nullable): how many requests were refused.
+ * With outputs apart from the inputs, a second call with the same inputs gives
+ * the same results.  Pointers are 4-byte aligned.  Limits: B <= 2^20, pages *
+ * page_size and max_pages * page_size below 2^31.
+ */
+sru_status sru_cache_extend(const int32_t* lengths, const int32_t* new_tokens, int32_t* table, int32_t* free_pages,
+                            const int32_t* free_count, int64_t B, int64_t max_pages, int64_t pages, int64_t page_size,
+                            int64_t T, int32_t* lengths_out, int32_t* free_count_out, int32_t* offsets,
+                            int32_t* slots, int32_t* refused, void* stream);
+
+/*
+ * Row r of K and V (T rows of Hkv * D elements of type t, F32 or BF16, k_ld and
+ * v_ld elements apart, e.g. the two halves of [K | V]) to slot slots[r] of the
+ * caches, rounded to bf16.  A negative slot writes nothing; one >= pages *
+ * page_size writes nothing and is reported as SRU_ERR_INVALID by the next
+ * sru_sync_status().  Of two rows with the same slot either may win, element by
+ * element.  Limits: D % 8 == 0; k_ld, v_ld multiples of 16 bytes; K, V and the
+ * caches 16-byte aligned.
+ */
+sru_status sru_cache_append(const void* K, int64_t k_ld, const void* V, int64_t v_ld, int t, const int32_t* slots,
+                            void* k_cache, void* v_cache, int64_t T, int64_t Hkv, int64_t D, int64_t page_size,
+                            int64_t pages, void* stream);
+
+/*
+ * Attention of one new token per request over the paged cache: the single-token
+ * form of SRU++'s A = softmax(Q K^T / sqrt(d')) V (sru_attention_project), with
+ * Hq query heads that share Hkv key/value heads in groups of Hq / Hkv:
+ *   out[b][i] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q[b][i] . k_j)
+ * over the keys j of head i / (Hq / Hkv) with max(0, lengths[b] - window) <= j <
+ * lengths[b] (window = 0: all of them; lengths counts the new token when its row
+ * was appended first).  A request without keys gets out = 0 and lse = -inf.
+ *   q (B, Hq, D) bf16;  out (B, Hq, D) of type out_t (F32 or BF16), apart from q
+ *   lse (B, Hq) fp32, nullable: log sum_j p_j
+ * Scores, sums and the result are fp32; p enters the product with v in 16 bits
+ * of precision.  A page index outside [0, pages) leaves its keys out, a length
+ * beyond max_pages * page_size is cut there; both are reported as SRU_ERR_INVALID
+ * by the next sru_sync_status().
+ * workspace: >= sru_attention_decode_workspace_bytes(B, Hq, Hkv, D) bytes; calls
+ * that may run at the same time need one each.  The sums' order depends on the
+ * lengths and sizes alone: the same bits every run.
+ * Limits: D % 8 == 0, D <= 1024, Hq a multiple of Hkv, B <= 2^20, pages *
+ * page_size and max_pages * page_size below 2^31.  Negative lengths count as 0.
+ */
+size_t sru_attention_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
+sru_status sru_attention_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* table,
+                                const int32_t* lengths, void* out, int out_t, float* lse, int64_t B, int64_t Hq,
+                                int64_t Hkv, int64_t D, int64_t page_size, int64_t pages, int64_t max_pages,
+                                int64_t window, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, then read and clear the device error word of the
  * current device: SRU_ERR_TIMEOUT if a bounded wait expired since the last
  * call, SRU_ERR_INVALID if a kernel met an index out of range in its data (it

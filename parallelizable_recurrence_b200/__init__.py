@@ -38,7 +38,9 @@ EXPORTED = ("sru_status_string", "sru_get_last_cuda_error", "sru_version", "sru_
             "sru_attention_workspace_bytes",
             "sru_attention_project", "sru_attention_backward_workspace_bytes", "sru_attention_project_backward",
             "sru_decode_workspace_bytes", "sru_decode_step",
-            "sru_softmax_loss_workspace_bytes", "sru_softmax_loss", "sru_softmax_loss_backward", "sru_sync_status")
+            "sru_softmax_loss_workspace_bytes", "sru_softmax_loss", "sru_softmax_loss_backward",
+            "sru_cache_extend", "sru_cache_append", "sru_attention_decode_workspace_bytes", "sru_attention_decode",
+            "sru_sync_status")
 
 
 class SRUError(RuntimeError):
@@ -118,6 +120,16 @@ def load_library(path: str = LIB_PATH):
     lib.sru_softmax_loss_backward.restype = _int
     lib.sru_softmax_loss_backward.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _int, _i64, _i64, _i64,
                                               _vp, ctypes.c_size_t, _vp]
+    lib.sru_cache_extend.restype = _int
+    lib.sru_cache_extend.argtypes = [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp,
+                                     _vp]
+    lib.sru_cache_append.restype = _int
+    lib.sru_cache_append.argtypes = [_vp, _i64, _vp, _i64, _int, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _vp]
+    lib.sru_attention_decode_workspace_bytes.restype = ctypes.c_size_t
+    lib.sru_attention_decode_workspace_bytes.argtypes = [_i64, _i64, _i64, _i64]
+    lib.sru_attention_decode.restype = _int
+    lib.sru_attention_decode.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _i64, _i64, _i64, _i64, _i64, _i64,
+                                         _i64, _i64, _f32, _vp, ctypes.c_size_t, _vp]
     lib.sru_sync_status.restype = _int
     lib.sru_sync_status.argtypes = [_vp]
     _lib = lib
@@ -444,6 +456,92 @@ def sru_softmax_loss_backward(H, W, targets, lse, dloss, dH=None, dW=None, works
             SRU_F32 if dW is None else _dtype_code(dW), M, V, K, _ptr(workspace), _nbytes(workspace),
             _stream(stream)), "sru_softmax_loss_backward")
     return dH, dW
+
+
+def sru_cache_extend(lengths, new_tokens, block_table, free_pages, free_count, page_size: int, lengths_out,
+                     free_count_out, offsets, slots, refused=None, stream=None):
+    """Page bookkeeping of one serving step (see sru.h), all on the GPU.  Request b
+    holds lengths[b] tokens and brings new_tokens[b] more, or leaves (negative).
+    Pages of leaving requests go onto the stack free_pages[:free_count], pages for
+    new tokens come off it, in request order.  All tensors int32: lengths,
+    new_tokens, lengths_out (B,), block_table (B, max_pages), free_pages (pages,),
+    free_count, free_count_out, refused (1,), offsets (B + 1,), slots (T,).
+    block_table and free_pages are updated in place; lengths_out and free_count_out
+    may be lengths and free_count."""
+    lib = load_library()
+    B, maxp = block_table.shape
+    one = [free_count, free_count_out] + ([] if refused is None else [refused])
+    if any(tuple(t.shape) != (B,) for t in (lengths, new_tokens, lengths_out)) or any(t.numel() != 1 for t in one) \
+            or offsets.numel() != B + 1 or free_pages.dim() != 1 or slots.dim() != 1:
+        raise ValueError("shape mismatch")
+    i32 = torch.int32
+    with _same_device(lengths, new_tokens, block_table, free_pages, free_count, lengths_out, free_count_out, offsets,
+                      slots, refused):
+        _check(lib.sru_cache_extend(_ptr(lengths, i32), _ptr(new_tokens, i32), _ptr(block_table, i32),
+                                    _ptr(free_pages, i32), _ptr(free_count, i32), B, maxp, free_pages.numel(),
+                                    page_size, slots.numel(), _ptr(lengths_out, i32), _ptr(free_count_out, i32),
+                                    _ptr(offsets, i32), _ptr(slots, i32), _ptr(refused, i32), _stream(stream)),
+               "sru_cache_extend")
+    return lengths_out, offsets, slots
+
+
+def _row_strided(t: torch.Tensor, H: int, D: int):
+    """Pointer and row pitch of (T, H, D) rows that are packed within a row."""
+    if not t.is_cuda:
+        raise ValueError("tensor must live on a CUDA device")
+    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+        raise ValueError("the heads of a row must be contiguous")
+    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else H * D
+
+
+def sru_cache_append(K, V, slots, k_cache, v_cache, stream=None):
+    """Rows of K and V (T, Hkv, D), bf16 or fp32, to the slots (T,) int32 of the caches
+    (pages, Hkv, page_size, D) bf16; a negative slot writes nothing.  K and V may be
+    views of a wider matrix (rows any multiple of 16 bytes apart)."""
+    lib = load_library()
+    T, H, D = K.shape
+    pages, Hc, ps, Dc = k_cache.shape
+    if K.shape != V.shape or K.dtype != V.dtype or (Hc, Dc) != (H, D) or k_cache.shape != v_cache.shape \
+            or tuple(slots.shape) != (T,):
+        raise ValueError("shape mismatch")
+    with _same_device(K, V, slots, k_cache, v_cache):
+        (kp, k_ld), (vp, v_ld) = _row_strided(K, H, D), _row_strided(V, H, D)
+        _check(lib.sru_cache_append(kp, k_ld, vp, v_ld, _dtype_code(K), _ptr(slots, torch.int32),
+                                    _ptr(k_cache, torch.bfloat16), _ptr(v_cache, torch.bfloat16), T, H, D, ps, pages,
+                                    _stream(stream)), "sru_cache_append")
+    return k_cache, v_cache
+
+
+def sru_attention_decode_workspace_bytes(B: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(load_library().sru_attention_decode_workspace_bytes(B, Hq, Hkv, D))
+
+
+def sru_attention_decode(q, k_cache, v_cache, block_table, lengths, out, scale: Optional[float] = None,
+                         window: int = 0, lse=None, workspace=None, stream=None):
+    """Attention of one new token per request over the paged cache (see sru.h): q
+    (B, Hq, D) bf16, caches (pages, Hkv, page_size, D) bf16, block_table
+    (B, max_pages) and lengths (B,) int32, out (B, Hq, D) bf16 or fp32, written in
+    place, lse (B, Hq) fp32 or None.  scale defaults to D ** -0.5; window > 0 limits
+    each request to its last `window` keys.  A workspace of
+    sru_attention_decode_workspace_bytes(B, Hq, Hkv, D) bytes is allocated when none
+    is given."""
+    lib = load_library()
+    B, Hq, D = q.shape
+    pages, Hkv, ps, Dc = k_cache.shape
+    if Dc != D or k_cache.shape != v_cache.shape or out.shape != q.shape or block_table.dim() != 2 \
+            or block_table.shape[0] != B or tuple(lengths.shape) != (B,) \
+            or (lse is not None and tuple(lse.shape) != (B, Hq)):
+        raise ValueError("shape mismatch")
+    with _same_device(q, k_cache, v_cache, block_table, lengths, out, lse, workspace):
+        if workspace is None:
+            workspace = _scratch(sru_attention_decode_workspace_bytes(B, Hq, Hkv, D), q.device, stream)
+        _check(lib.sru_attention_decode(_ptr(q, torch.bfloat16), _ptr(k_cache, torch.bfloat16),
+                                        _ptr(v_cache, torch.bfloat16), _ptr(block_table, torch.int32),
+                                        _ptr(lengths, torch.int32), _ptr(out), _dtype_code(out),
+                                        _ptr(lse, torch.float32), B, Hq, Hkv, D, ps, pages, block_table.shape[1],
+                                        window, D ** -0.5 if scale is None else float(scale), _ptr(workspace),
+                                        _nbytes(workspace), _stream(stream)), "sru_attention_decode")
+    return out
 
 
 def sru_sync_status(stream=None) -> int:

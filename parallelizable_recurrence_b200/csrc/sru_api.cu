@@ -19,6 +19,8 @@
 #include "sru_scan.cuh"
 #include "sru_fused.cuh"
 #include "sru_loss.cuh"
+#include "sru_cache.cuh"
+#include "sru_cache_attention.cuh"
 
 namespace {
 
@@ -1933,6 +1935,165 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
         }
     }
     if (dH && h_in_slabs) return sum_slabs(slab_h, dH, dh_t, M, K, p.dh.slab_rows, p.dh.splits, st);
+    return SRU_OK;
+}
+
+// ---- paged key/value cache and the attention of one new token over it
+static sru_status check_cache_sizes(int64_t pages, int64_t ps) {
+    if (pages < 0 || ps < 1) return SRU_ERR_INVALID;
+    if (pages >= ((int64_t)1 << 31) || ps >= ((int64_t)1 << 31) || pages * ps >= ((int64_t)1 << 31))
+        return SRU_ERR_UNSUPPORTED;
+    return SRU_OK;
+}
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// New rows above which the step's bookkeeping runs on a cluster of 8 CTAs.
+constexpr int64_t kExtendClusterRows = 8192;
+
+sru_status sru_cache_extend(const int32_t* lengths, const int32_t* new_tokens, int32_t* table, int32_t* free_pages,
+                            const int32_t* free_count, int64_t B, int64_t max_pages, int64_t pages, int64_t page_size,
+                            int64_t T, int32_t* lengths_out, int32_t* free_count_out, int32_t* offsets,
+                            int32_t* slots, int32_t* refused, void* stream) {
+    sru_status s = check_cache_sizes(pages, page_size);
+    if (s == SRU_OK) s = check_cache_sizes(max_pages, page_size);
+    if (s != SRU_OK) return s;
+    if (B < 0 || T < 0) return SRU_ERR_INVALID;
+    if (B > ((int64_t)1 << 20) || T >= ((int64_t)1 << 31)) return SRU_ERR_UNSUPPORTED;
+    if (!free_count || !free_count_out || !offsets || (T > 0 && !slots) || (pages > 0 && !free_pages) ||
+        (B > 0 && (!lengths || !new_tokens || !lengths_out || (max_pages > 0 && !table))))
+        return SRU_ERR_INVALID;
+    const void* ptrs[] = {lengths, new_tokens, table, free_pages, free_count, lengths_out, free_count_out,
+                          offsets, slots, refused};
+    for (const void* p : ptrs)
+        if (!aligned4(p)) return SRU_ERR_INVALID;
+    sru::cache::ExtendArgs a{lengths,     new_tokens,     table,   free_pages, free_count, lengths_out,
+                             free_count_out, offsets,     slots,   refused,    (int)B,     (int)max_pages,
+                             (int)pages,  (int)page_size, (int)T};
+    const unsigned ctas = T > kExtendClusterRows ? 8 : 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(sru::cache::kExtThreads);
+    cfg.stream = as_stream(stream);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    SRU_CUDA_TRY(cudaLaunchKernelEx(&cfg, sru::cache::cache_extend_kernel, a));
+    return SRU_OK;
+}
+
+sru_status sru_cache_append(const void* K, int64_t k_ld, const void* V, int64_t v_ld, int t, const int32_t* slots,
+                            void* k_cache, void* v_cache, int64_t T, int64_t Hkv, int64_t D, int64_t page_size,
+                            int64_t pages, void* stream) {
+    sru_status s = check_cache_sizes(pages, page_size);
+    if (s != SRU_OK) return s;
+    if (T < 0 || Hkv < 1 || D < 1 || (t != SRU_F32 && t != SRU_BF16)) return SRU_ERR_INVALID;
+    const int64_t lim = (int64_t)1 << 31;
+    if (T >= lim || Hkv >= lim || D >= lim || Hkv * D >= lim) return SRU_ERR_UNSUPPORTED;
+    const int64_t unit = t == SRU_BF16 ? 8 : 4;  // elements of 16 bytes
+    if (D % 8 != 0) return SRU_ERR_UNSUPPORTED;
+    if (T > 1 && (k_ld < Hkv * D || v_ld < Hkv * D)) return SRU_ERR_INVALID;
+    if (T > 1 && (k_ld % unit != 0 || v_ld % unit != 0)) return SRU_ERR_UNSUPPORTED;
+    if (T == 0) return SRU_OK;
+    if (!K || !V || !slots || !aligned16(K) || !aligned16(V) || !aligned4(slots)) return SRU_ERR_INVALID;
+    if (pages > 0 && (!k_cache || !v_cache)) return SRU_ERR_INVALID;
+    if (!aligned16(k_cache) || !aligned16(v_cache)) return SRU_ERR_INVALID;
+    const size_t items = (size_t)T * (Hkv * D / 8);
+    const dim3 grid((unsigned)std::min<size_t>(blocks_for(std::min<size_t>(items, (size_t)1 << 38), 256),
+                                               (size_t)sm_count() * 32),
+                    2);
+    __nv_bfloat16 *kc = static_cast<__nv_bfloat16*>(k_cache), *vc = static_cast<__nv_bfloat16*>(v_cache);
+    if (t == SRU_BF16)
+        sru::cache::cache_append_kernel<<<grid, 256, 0, as_stream(stream)>>>(
+            static_cast<const __nv_bfloat16*>(K), (long long)k_ld, static_cast<const __nv_bfloat16*>(V),
+            (long long)v_ld, slots, kc, vc, (int)T, (int)Hkv, (int)D, (int)page_size, (long long)(pages * page_size));
+    else
+        sru::cache::cache_append_kernel<<<grid, 256, 0, as_stream(stream)>>>(
+            static_cast<const float*>(K), (long long)k_ld, static_cast<const float*>(V), (long long)v_ld, slots, kc,
+            vc, (int)T, (int)Hkv, (int)D, (int)page_size, (long long)(pages * page_size));
+    SRU_CUDA_TRY(cudaGetLastError());
+    return SRU_OK;
+}
+
+constexpr int64_t kDecodeMaxD = (int64_t)sru::cache::kSlice * sru::cache::kMaxWarps;
+struct DecodePlan {
+    int tw, teams, slice, blocks;
+    size_t jobs_off, range_off, total;
+};
+static DecodePlan decode_plan(int64_t Hq, int64_t Hkv, int64_t D) {
+    DecodePlan p{};
+    p.tw = (int)((D + sru::cache::kSlice - 1) / sru::cache::kSlice);
+    p.teams = sru::cache::kMaxWarps / p.tw;
+    p.slice = (int)(((D + p.tw - 1) / p.tw + 15) / 16 * 16);
+    p.blocks = (int)((Hq / Hkv + 7) / 8);
+    const size_t teams = (size_t)sm_count() * p.teams;
+    p.jobs_off = round256(teams * 2 * sru::cache::piece_floats(8, p.tw * p.slice) * sizeof(float));
+    p.range_off = p.jobs_off + round256(teams * sizeof(int4));
+    p.total = p.range_off + 256;
+    return p;
+}
+static sru_status check_decode_sizes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+    if (B < 0 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv != 0) return SRU_ERR_INVALID;
+    if (D % 8 != 0 || D > kDecodeMaxD || B > ((int64_t)1 << 20) || Hq > 65536) return SRU_ERR_UNSUPPORTED;
+    return SRU_OK;
+}
+
+size_t sru_attention_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
+    return check_decode_sizes(B, Hq, Hkv, D) == SRU_OK ? decode_plan(Hq, Hkv, D).total : 0;
+}
+
+sru_status sru_attention_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* table,
+                                const int32_t* lengths, void* out, int out_t, float* lse, int64_t B, int64_t Hq,
+                                int64_t Hkv, int64_t D, int64_t page_size, int64_t pages, int64_t max_pages,
+                                int64_t window, float scale, void* workspace, size_t workspace_bytes, void* stream) {
+    sru_status s = check_decode_sizes(B, Hq, Hkv, D);
+    if (s == SRU_OK) s = check_cache_sizes(pages, page_size);
+    if (s == SRU_OK) s = check_cache_sizes(max_pages, page_size);
+    if (s != SRU_OK) return s;
+    if (window < 0 || (out_t != SRU_F32 && out_t != SRU_BF16)) return SRU_ERR_INVALID;
+    if (B == 0) return SRU_OK;
+    if (!q || !lengths || !out || !workspace || (max_pages > 0 && !table) || (pages > 0 && (!k_cache || !v_cache)))
+        return SRU_ERR_INVALID;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace) ||
+        !aligned4(table) || !aligned4(lengths) || !aligned4(lse))
+        return SRU_ERR_INVALID;
+    const DecodePlan p = decode_plan(Hq, Hkv, D);
+    if (workspace_bytes < p.total) return SRU_ERR_INVALID;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    sru::cache::DecodeArgs a{};
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.k = static_cast<const __nv_bfloat16*>(k_cache);
+    a.v = static_cast<const __nv_bfloat16*>(v_cache);
+    a.table = table;
+    a.lengths = lengths;
+    a.out = out;
+    a.lse = lse;
+    a.part = reinterpret_cast<float*>(ws);
+    a.jobs = reinterpret_cast<int4*>(ws + p.jobs_off);
+    a.range = reinterpret_cast<long long*>(ws + p.range_off);
+    a.B = (int)B; a.Hq = (int)Hq; a.Hkv = (int)Hkv; a.D = (int)D;
+    if (pages == 0) max_pages = 0;  // no key can be read
+    a.ps = (int)page_size; a.maxp = (int)max_pages; a.pages = (int)pages;
+    a.window = (int)std::min<int64_t>(window, INT32_MAX);
+    a.out_f32 = out_t == SRU_F32;
+    a.group = (int)(Hq / Hkv);
+    a.blocks = p.blocks; a.tw = p.tw; a.teams = p.teams; a.slice = p.slice;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    cudaStream_t st = as_stream(stream);
+    const int threads = p.tw * p.teams * 32;
+    const size_t smem = (size_t)p.tw * p.teams * sru::cache::kRingBytes;
+    SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(sru::cache::cache_attention_kernel),
+                             (size_t)sru::cache::kMaxWarps * sru::cache::kRingBytes));
+    // no more teams than there can be steps
+    const int64_t steps = B * Hkv * p.blocks * ((max_pages * page_size + sru::cache::kStep - 1) / sru::cache::kStep);
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((steps + p.teams - 1) / p.teams, sm_count()));
+    sru::cache::cache_attention_kernel<<<(unsigned)grid, threads, smem, st>>>(a);
+    SRU_CUDA_TRY(cudaGetLastError());
+    const dim3 jgrid((unsigned)(grid * p.teams), (unsigned)std::min<int64_t>(8, Hq / Hkv), (unsigned)((D + 127) / 128));
+    sru::cache::cache_join_kernel<<<jgrid, sru::cache::kJoinThreads, 0, st>>>(a);
+    SRU_CUDA_TRY(cudaGetLastError());
     return SRU_OK;
 }
 
