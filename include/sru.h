@@ -462,8 +462,10 @@ sru_status sru_cache_append(const void* K, int64_t k_ld, const void* V, int64_t 
  * workspace: >= sru_attention_decode_workspace_bytes(B, Hq, Hkv, D) bytes; calls
  * that may run at the same time need one each.  The sums' order depends on the
  * lengths and sizes alone: the same bits every run.
- * Limits: D % 8 == 0, D <= 1024, Hq a multiple of Hkv, B <= 2^20, pages *
- * page_size and max_pages * page_size below 2^31.  Negative lengths count as 0.
+ * Limits: D % 8 == 0, D <= 1024, Hq a multiple of Hkv, B <= 2^20, pages * Hkv,
+ * pages * page_size and max_pages * page_size below 2^31.  Negative lengths count
+ * as 0.  Any page size works; the cache is read in boxes of rows as long as the
+ * largest power of two (up to 32) that divides it, so odd sizes are slow.
  */
 size_t sru_attention_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D);
 sru_status sru_attention_decode(const void* q, const void* k_cache, const void* v_cache, const int32_t* table,

@@ -2019,19 +2019,17 @@ sru_status sru_cache_append(const void* K, int64_t k_ld, const void* V, int64_t 
 
 constexpr int64_t kDecodeMaxD = (int64_t)sru::cache::kSlice * sru::cache::kMaxWarps;
 struct DecodePlan {
-    int tw, teams, slice, blocks;
-    size_t jobs_off, range_off, total;
+    int tw, teams, blocks;
+    size_t jobs_off, total;
 };
 static DecodePlan decode_plan(int64_t Hq, int64_t Hkv, int64_t D) {
     DecodePlan p{};
     p.tw = (int)((D + sru::cache::kSlice - 1) / sru::cache::kSlice);
     p.teams = sru::cache::kMaxWarps / p.tw;
-    p.slice = (int)(((D + p.tw - 1) / p.tw + 15) / 16 * 16);
     p.blocks = (int)((Hq / Hkv + 7) / 8);
     const size_t teams = (size_t)sm_count() * p.teams;
-    p.jobs_off = round256(teams * 2 * sru::cache::piece_floats(8, p.tw * p.slice) * sizeof(float));
-    p.range_off = p.jobs_off + round256(teams * sizeof(int4));
-    p.total = p.range_off + 256;
+    p.jobs_off = round256(teams * 2 * sru::cache::piece_floats(8, p.tw * sru::cache::kSlice) * sizeof(float));
+    p.total = p.jobs_off + round256(teams * sizeof(int4));
     return p;
 }
 static sru_status check_decode_sizes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
@@ -2053,6 +2051,7 @@ sru_status sru_attention_decode(const void* q, const void* k_cache, const void* 
     if (s == SRU_OK) s = check_cache_sizes(max_pages, page_size);
     if (s != SRU_OK) return s;
     if (window < 0 || (out_t != SRU_F32 && out_t != SRU_BF16)) return SRU_ERR_INVALID;
+    if (pages * Hkv >= ((int64_t)1 << 31)) return SRU_ERR_UNSUPPORTED;
     if (B == 0) return SRU_OK;
     if (!q || !lengths || !out || !workspace || (max_pages > 0 && !table) || (pages > 0 && (!k_cache || !v_cache)))
         return SRU_ERR_INVALID;
@@ -2072,24 +2071,37 @@ sru_status sru_attention_decode(const void* q, const void* k_cache, const void* 
     a.lse = lse;
     a.part = reinterpret_cast<float*>(ws);
     a.jobs = reinterpret_cast<int4*>(ws + p.jobs_off);
-    a.range = reinterpret_cast<long long*>(ws + p.range_off);
     a.B = (int)B; a.Hq = (int)Hq; a.Hkv = (int)Hkv; a.D = (int)D;
     if (pages == 0) max_pages = 0;  // no key can be read
     a.ps = (int)page_size; a.maxp = (int)max_pages; a.pages = (int)pages;
     a.window = (int)std::min<int64_t>(window, INT32_MAX);
     a.out_f32 = out_t == SRU_F32;
     a.group = (int)(Hq / Hkv);
-    a.blocks = p.blocks; a.tw = p.tw; a.teams = p.teams; a.slice = p.slice;
+    a.blocks = p.blocks; a.tw = p.tw; a.teams = p.teams;
+    a.box_rows = (int)std::min<int64_t>(page_size & -page_size, sru::cache::kStep);
     a.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t st = as_stream(stream);
     const int threads = p.tw * p.teams * 32;
-    const size_t smem = (size_t)p.tw * p.teams * sru::cache::kRingBytes;
+    const size_t smem = (size_t)p.tw * p.teams * sru::cache::kRingBytes + 1024;
     SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(sru::cache::cache_attention_kernel),
-                             (size_t)sru::cache::kMaxWarps * sru::cache::kRingBytes));
+                             (size_t)sru::cache::kMaxWarps * sru::cache::kRingBytes + 1024));
+    // the caches as (D, page_size, pages * Hkv), in boxes of 64 features x box_rows rows of
+    // one page; without pages nothing is loaded through them
+    CUtensorMap mk{}, mv{};
+    if (pages > 0) {
+        const uint64_t dims[3] = {(uint64_t)D, (uint64_t)page_size, (uint64_t)(pages * Hkv)};
+        const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)(page_size * D) * 2};
+        const uint32_t box[3] = {64, (uint32_t)a.box_rows, 1};
+        if (!make_map(&mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_cache, dims, strides, box,
+                      CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !make_map(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v_cache, dims, strides, box,
+                      CU_TENSOR_MAP_SWIZZLE_128B))
+            return SRU_ERR_INVALID;
+    }
     // no more teams than there can be steps
     const int64_t steps = B * Hkv * p.blocks * ((max_pages * page_size + sru::cache::kStep - 1) / sru::cache::kStep);
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((steps + p.teams - 1) / p.teams, sm_count()));
-    sru::cache::cache_attention_kernel<<<(unsigned)grid, threads, smem, st>>>(a);
+    sru::cache::cache_attention_kernel<<<(unsigned)grid, threads, smem, st>>>(mk, mv, a);
     SRU_CUDA_TRY(cudaGetLastError());
     const dim3 jgrid((unsigned)(grid * p.teams), (unsigned)std::min<int64_t>(8, Hq / Hkv), (unsigned)((D + 127) / 128));
     sru::cache::cache_join_kernel<<<jgrid, sru::cache::kJoinThreads, 0, st>>>(a);

@@ -15,14 +15,16 @@
 // spans teams leaves its pieces (m, l, unnormalised o, fp32) in the workspace
 // and cache_join_kernel joins them.
 //
-// A team is TW = ceil(D / 128) warps; warp w owns the feature slice w of q, k, v
-// and o (at most 128 wide), loads it itself (cp.async, kStages steps of 16 x 2 rows,
-// no barrier with other warps), multiplies on the tensor cores with the keys as
-// rows -- S^T = K Q^T (16 keys x 8 heads), O^T = V^T P^T (16 features x 8 heads) --
-// and only the 16 x 8 partial scores cross the team's warps, through shared
-// memory.  p goes to the tensor cores as two bf16 parts (value and remainder, 16
-// bits together), so o is as exact as fp32 scores make it; the second product is
-// free next to the loads.
+// A team is TW = ceil(D / 128) warps; warp w owns features 128 w .. of q, k, v and
+// o.  It loads its part itself, by TMA: units of 32 rows x 128 features, K and V in
+// turn, through a ring of its own whose barriers no other warp touches.  A page
+// of ps tokens allows boxes of R rows, R the largest power of two (<= 32) that
+// divides ps.  Keys are rows of the tensor-core products -- S^T = K Q^T (16 keys x
+// 8 heads), O^T = V^T P^T (16 features x 8 heads) -- so a group of up to 8 heads
+// costs what one does, and only the 32 x 8 partial scores cross the team's warps,
+// through shared memory.  p enters its product as two bf16 parts (value and
+// remainder, 16 bits together), so o is as exact as fp32 scores make it; the second
+// product is free next to the loads.
 #pragma once
 
 #include "sru_ptx.cuh"
@@ -30,13 +32,12 @@
 namespace sru {
 namespace cache {
 
-constexpr int kStep = 16;     // keys per step
-constexpr int kStages = 3;    // steps in a warp's ring
+constexpr int kStep = 32;     // keys per step
 constexpr int kSlice = 128;   // features per warp
 constexpr int kMaxWarps = 8;  // per CTA
-constexpr uint32_t kRowBytes = kSlice * 2;
-constexpr uint32_t kStageBytes = 2 * kStep * kRowBytes;  // K and V rows
-constexpr uint32_t kRingBytes = kStages * kStageBytes;
+constexpr uint32_t kHalfBytes = kStep * 128;       // 64 features of a step's rows
+constexpr uint32_t kRingBytes = 6 * kHalfBytes;    // per warp: 3 units, or 6 of one half when D <= 64
+constexpr int kMaxUnits = 6, kMasks = 4;
 
 struct DecodeArgs {
     const __nv_bfloat16 *q, *k, *v;
@@ -45,30 +46,21 @@ struct DecodeArgs {
     float* lse;          // nullable
     float* part;         // pieces: team * 2 + (1 = starts its item, 0 = goes on with it)
     int4* jobs;          // per team: the item that it starts and does not finish
-    long long* range;    // steps per team
     int B, Hq, Hkv, D, ps, maxp, pages, window, out_f32;
     int group;           // query heads per key head
     int blocks;          // head blocks per key head
     int tw, teams;       // warps per team, teams per CTA
-    int slice;           // features per warp (a multiple of 16)
+    int box_rows;        // R
     float scale_log2;    // scale * log2 e
 };
 
-// floats of one piece: o [heads][tw * slice], then m and l [heads]
+// floats of one piece: o [heads][tw * kSlice], then m and l [heads]
 __host__ __device__ inline size_t piece_floats(int heads, int dp) { return (size_t)heads * dp + 2 * heads; }
 
 __device__ __forceinline__ float ex2f(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -134,16 +126,27 @@ struct Cursor {
     }
 };
 
-__global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_attention_kernel(DecodeArgs a) {
-    extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ float4 exch[2][kMaxWarps][32];
-    __shared__ uint32_t s_mask[kMaxWarps][kStages];
-    __shared__ long long s_scan[kMaxWarps];
+__global__ void __launch_bounds__(kMaxWarps * 32, 1)
+    cache_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                           DecodeArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ float4 exch[2][kMaxWarps][2][32];
+    __shared__ uint64_t s_full[kMaxWarps][kMaxUnits];
+    __shared__ uint32_t s_mask[kMaxWarps][kMasks];
+    __shared__ long long s_scan[kMaxWarps], s_rem[kMaxWarps];
     __shared__ int s_b[kMaxWarps];
-    __shared__ long long s_rem[kMaxWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthreads = blockDim.x;
     const int HH = a.Hkv * a.blocks;
 
+    if (lane == 0) {
+        for (int i = 0; i < kMaxUnits; ++i) mbar_init(&s_full[warp][i], 1);
+        fence_mbar_init();
+    }
+    if (tid == 0) {
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+    }
     // ---- this CTA's teams' places in the list: sums of steps over the requests
     const int per_thread = (a.B + nthreads - 1) / nthreads;
     long long mine = 0;
@@ -158,10 +161,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_attention_kernel(Deco
         if (lane >= o) upto += u;
     }
     if (lane == 31) s_scan[warp] = upto;
-    for (int i = tid; i < a.teams; i += nthreads) s_b[i] = a.B;
-    // stale features behind D stay zero: loads never touch them
-    for (uint32_t i = tid; i < (nthreads / 32) * kRingBytes / 16; i += nthreads)
-        reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     long long total = 0, before = upto - mine;
     for (int w = 0; w < nthreads / 32; ++w) {
@@ -170,7 +169,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_attention_kernel(Deco
     }
     const long long n_teams = (long long)gridDim.x * a.teams;
     const long long per = max(1ll, (total + n_teams - 1) / n_teams);
-    if (blockIdx.x == 0 && tid == 0) *a.range = per;
     for (int t = 0; t < a.teams; ++t) {
         const long long g0 = ((long long)blockIdx.x * a.teams + t) * per;
         if (g0 >= before && g0 < before + mine) {
@@ -202,7 +200,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_attention_kernel(Deco
     __syncthreads();
 
     const int team = warp / a.tw, w_in = warp - team * a.tw;
-    if (team >= a.teams) return;
     const long long my_team = (long long)blockIdx.x * a.teams + team;
     const long long g0 = my_team * per, g1 = min(total, g0 + per);
     if (g0 >= g1) {
@@ -219,68 +216,86 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_attention_kernel(Deco
     }
     Cursor ld = cur;
 
-    const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
-    const int f0 = w_in * a.slice;                         // first feature of this warp
-    const int width = min(a.slice, a.D - f0);              // features (D % 8 == 0), may be <= 0
-    const int chunks = max(0, width) / 8;                  // 16-byte chunks of a row
-    const int my_chunk = lane & 15, my_row = lane >> 4;
+    const int f0 = w_in * kSlice;                   // first feature of this warp
+    const int width = min(kSlice, a.D - f0);        // its features, a multiple of 8
+    const int halves = width > 64 ? 2 : 1;          // boxes of 64 features
+    const int n_units = a.D > 64 ? 3 : 6;
+    const uint32_t unit_bytes = a.D > 64 ? 2 * kHalfBytes : kHalfBytes;
+    uint8_t* ring = smem + warp * kRingBytes;
+    const int R = a.box_rows, groups = kStep / R;
+    const int my_group = lane & (groups - 1), my_half = lane / groups;  // boxes of this lane: my_half, + 32 / groups
 
-    // table entry and row of key (lane & 15) of step `ld`: the entry is read one step
-    // before its load, so that its latency is not waited for
-    int next_page = 0, next_in = -1;  // next_in < 0: no such key
-    auto fetch_row = [&]() {
-        const int pos = ld.s * kStep + (lane & 15);
+    // Table entry of this lane's box of step `ld`: read one step before its load, so
+    // that its latency is not waited for.
+    int next_page = 0, next_in = -1;  // next_in < 0: no key of the box is wanted
+    auto fetch_page = [&]() {
+        const int pos = ld.s * kStep + my_group * R;
         next_in = -1;
-        if (pos >= ld.sp.lo && pos < ld.sp.hi) {
+        if (pos + R > ld.sp.lo && pos < ld.sp.hi) {
             const int p = pos / a.ps;
             next_page = __ldg(a.table + (size_t)ld.b * a.maxp + p);
             next_in = pos - p * a.ps;
         }
     };
-    auto load = [&](int stage) {
-        const uint32_t st = ring + stage * kStageBytes;
-        bool there = next_in >= 0;
-        if (there && (unsigned)next_page >= (unsigned)a.pages) {
-            record_error(kErrBadIndex);  // the key is left out
-            there = false;
-        }
-        const long long next_row = ((long long)next_page * a.Hkv + ld.hh / a.blocks) * a.ps + next_in;
-        const unsigned mask = __ballot_sync(0xffffffffu, there) & 0xffffu;
-        if (lane == 0) s_mask[warp][stage] = mask;
-#pragma unroll
-        for (int j = 0; j < kStep / 2; ++j) {
-            const int r = 2 * j + my_row;
-            const long long row = __shfl_sync(0xffffffffu, next_row, r);
-            if (my_chunk < chunks) {
-                const bool live = (mask >> r) & 1;
-                const size_t at = live ? (size_t)row * a.D + f0 + my_chunk * 8 : 0;
-                const uint32_t dst = st + r * kRowBytes + ((my_chunk ^ (r & 7)) << 4);
-                cp_async16(dst, a.k + at, live ? 16u : 0u);
-                cp_async16(dst + kStep * kRowBytes, a.v + at, live ? 16u : 0u);
+    int box_row = 0, box_in = -1;  // this lane's box of the step being loaded
+    uint32_t step_bytes = 0;
+    long long loaded = g0;         // step of the next unit to load
+    int load_unit = 0, load_stage = 0, mask_at = 0;  // load_unit: 0 = K, 1 = V
+    bool dead = false;             // a wait ran out: no further loads or waits
+    auto load_next = [&]() {
+        if (loaded >= g1 || dead) return;
+        uint64_t* bar = &s_full[warp][load_stage];
+        uint8_t* dst = ring + load_stage * unit_bytes;
+        if (load_unit == 0) {
+            box_in = next_in;
+            if (box_in >= 0 && (unsigned)next_page >= (unsigned)a.pages) {
+                record_error(kErrBadIndex);  // its keys are left out
+                box_in = -1;
             }
+            box_row = (int)((unsigned)next_page * a.Hkv + ld.hh / a.blocks);
+            const unsigned there = __ballot_sync(0xffffffffu, box_in >= 0) & (groups == 32 ? ~0u : (1u << groups) - 1);
+            step_bytes = __popc(there) * halves * R * 128;
+            const int pos = ld.s * kStep + lane;
+            const unsigned mask =
+                __ballot_sync(0xffffffffu, pos >= ld.sp.lo && pos < ld.sp.hi && ((there >> (lane / R)) & 1));
+            if (lane == 0) s_mask[warp][mask_at] = mask;
+            mask_at = (mask_at + 1) & (kMasks - 1);
         }
-    };
-    long long loaded = g0;
-    fetch_row();
-    auto load_next = [&](int stage) {
-        if (loaded < g1) {
-            load(stage);
-            if (++loaded < g1) {
-                ld.next(a);
-                fetch_row();
-            }
+        if (lane == 0) mbar_arrive_expect_tx(bar, step_bytes);
+        __syncwarp();
+        if (box_in >= 0)
+            for (int h = my_half; h < halves; h += 32 / groups)
+                tma_load_3d(dst + h * kHalfBytes + my_group * R * 128, load_unit ? &map_v : &map_k, bar, f0 + h * 64,
+                            box_in, box_row);
+        if (load_unit == 1 && ++loaded < g1) {
+            ld.next(a);
+            fetch_page();
         }
-        cp_commit();
+        load_unit ^= 1;
+        load_stage = load_stage + 1 == n_units ? 0 : load_stage + 1;
     };
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) load_next(i);
+    fetch_page();
+    for (int i = 0; i < n_units; ++i) load_next();
 
     const int g = lane >> 2, t2 = (lane & 3) * 2;
     uint32_t qf[kSlice / 16][2];
     float o[kSlice / 16][4];
     float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;  // heads t2, t2 + 1
     bool open = false, begins = false;
-    int stage = 0, buf = 0;
+    int stage = 0, buf = 0, mask_use = 0;
+    uint32_t phase = 0;
+    // this warp's next unit has landed (false: the wait ran out)
+    auto wait_unit = [&]() {
+        if (!dead && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][stage], phase, kErrTimeoutLoad))) dead = true;
+    };
+    auto unit_done = [&]() {
+        if (++stage == n_units) {
+            stage = 0;
+            phase ^= 1u;
+        }
+        __syncwarp();  // every lane has read the unit
+        load_next();
+    };
     for (long long step = g0; step < g1; ++step) {
         const int hblk = cur.hh % a.blocks, kv = cur.hh / a.blocks;
         const int head0 = kv * a.group + hblk * 8, heads = min(8, a.group - hblk * 8);
@@ -299,86 +314,118 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_attention_kernel(Deco
             m0 = m1 = -INFINITY;
             l0 = l1 = 0.f;
         }
-        load_next(stage == 0 ? kStages - 1 : stage - 1);
-        cp_wait<kStages - 1>();
-        __syncwarp();
-        const uint32_t ks = ring + stage * kStageBytes, vs = ks + kStep * kRowBytes;
-        float sc[4] = {0.f, 0.f, 0.f, 0.f}, sc2[4] = {0.f, 0.f, 0.f, 0.f};
+        // ---- scores of 2 x 16 keys
+        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        wait_unit();
         {
-            const int r = lane & 15, hi = lane >> 4;
+            const uint32_t base = smem_u32(ring) + stage * unit_bytes + (lane & 15) * 128;
+            const int r7 = lane & 7, hi = lane >> 4;
 #pragma unroll
             for (int kk = 0; kk < kSlice / 16; ++kk) {
                 if (kk * 16 >= width) break;
-                uint32_t kf[4];
-                ldsm4(ks + r * kRowBytes + (((2 * kk + hi) ^ (r & 7)) << 4), kf);
-                if (kk & 1) mma_bf16(sc2, kf, qf[kk][0], qf[kk][1]);
-                else mma_bf16(sc, kf, qf[kk][0], qf[kk][1]);
+                const uint32_t at = base + (kk >> 2) * kHalfBytes + (((2 * (kk & 3) + hi) ^ r7) << 4);
+                uint32_t ka[4], kb[4];
+                ldsm4(at, ka);
+                ldsm4(at + 16 * 128, kb);
+                mma_bf16(sc[0], ka, qf[kk][0], qf[kk][1]);
+                mma_bf16(sc[1], kb, qf[kk][0], qf[kk][1]);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[e] += sc2[e];
         }
+        unit_done();
         if (a.tw > 1) {
-            exch[buf][warp][lane] = make_float4(sc[0], sc[1], sc[2], sc[3]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) exch[buf][warp][i][lane] = make_float4(sc[i][0], sc[i][1], sc[i][2], sc[i][3]);
             team_sync(team, a.tw * 32);
-            float4 s = exch[buf][team * a.tw][lane];
-            for (int w = 1; w < a.tw; ++w) {
-                const float4 x = exch[buf][team * a.tw + w][lane];
-                s.x += x.x;
-                s.y += x.y;
-                s.z += x.z;
-                s.w += x.w;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float4 s = exch[buf][team * a.tw][i][lane];
+                for (int w = 1; w < a.tw; ++w) {
+                    const float4 x = exch[buf][team * a.tw + w][i][lane];
+                    s.x += x.x;
+                    s.y += x.y;
+                    s.z += x.z;
+                    s.w += x.w;
+                }
+                sc[i][0] = s.x;
+                sc[i][1] = s.y;
+                sc[i][2] = s.z;
+                sc[i][3] = s.w;
             }
-            sc[0] = s.x;
-            sc[1] = s.y;
-            sc[2] = s.z;
-            sc[3] = s.w;
             buf ^= 1;
         }
-        const uint32_t mask = s_mask[warp][stage];
-        const bool k0 = (mask >> g) & 1, k1 = (mask >> (g + 8)) & 1;
-        sc[0] = k0 ? sc[0] * a.scale_log2 : -INFINITY;
-        sc[1] = k0 ? sc[1] * a.scale_log2 : -INFINITY;
-        sc[2] = k1 ? sc[2] * a.scale_log2 : -INFINITY;
-        sc[3] = k1 ? sc[3] * a.scale_log2 : -INFINITY;
-        float n0 = fmaxf(sc[0], sc[2]), n1 = fmaxf(sc[1], sc[3]);
+        // ---- running maximum and sum; p of keys 16 i + g and + 8, heads t2 and t2 + 1
+        const uint32_t mask = s_mask[warp][mask_use];
+        mask_use = (mask_use + 1) & (kMasks - 1);
+        float n0 = m0, n1 = m1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool k0 = (mask >> (16 * i + g)) & 1, k1 = (mask >> (16 * i + g + 8)) & 1;
+            sc[i][0] = k0 ? sc[i][0] * a.scale_log2 : -INFINITY;
+            sc[i][1] = k0 ? sc[i][1] * a.scale_log2 : -INFINITY;
+            sc[i][2] = k1 ? sc[i][2] * a.scale_log2 : -INFINITY;
+            sc[i][3] = k1 ? sc[i][3] * a.scale_log2 : -INFINITY;
+            n0 = fmaxf(n0, fmaxf(sc[i][0], sc[i][2]));
+            n1 = fmaxf(n1, fmaxf(sc[i][1], sc[i][3]));
+        }
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
             n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
             n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
         }
-        n0 = fmaxf(n0, m0);
-        n1 = fmaxf(n1, m1);
         const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;  // nothing seen yet
         const float f0c = ex2f(m0 - b0), f1c = ex2f(m1 - b1);
         m0 = n0;
         m1 = n1;
-        float p[4] = {ex2f(sc[0] - b0), ex2f(sc[1] - b1), ex2f(sc[2] - b0), ex2f(sc[3] - b1)};
-        l0 = __fmaf_rn(l0, f0c, p[0] + p[2]);
-        l1 = __fmaf_rn(l1, f1c, p[1] + p[3]);
-        uint32_t ph[2], pl[2];
+        l0 *= f0c;
+        l1 *= f1c;
+        uint32_t ph[2][2], pl[2][2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            ph[i] = pack_bf16(p[2 * i], p[2 * i + 1]);
-            const float h0 = __uint_as_float(ph[i] << 16), h1 = __uint_as_float(ph[i] & 0xffff0000u);
-            pl[i] = movm(pack_bf16(p[2 * i] - h0, p[2 * i + 1] - h1));
-            ph[i] = movm(ph[i]);
+            const float p[4] = {ex2f(sc[i][0] - b0), ex2f(sc[i][1] - b1), ex2f(sc[i][2] - b0), ex2f(sc[i][3] - b1)};
+            l0 += p[0] + p[2];
+            l1 += p[1] + p[3];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t h = pack_bf16(p[2 * j], p[2 * j + 1]);
+                pl[i][j] = movm(pack_bf16(p[2 * j] - __uint_as_float(h << 16),
+                                          p[2 * j + 1] - __uint_as_float(h & 0xffff0000u)));
+                ph[i][j] = movm(h);
+            }
+        }
+        wait_unit();
+        if (mask != ~0u) {
+            // rows without a key hold what the page held (or the ring, where no box was
+            // loaded): p = 0 there must meet a finite value
+            if (!((mask >> lane) & 1)) {
+                uint8_t* row = ring + stage * unit_bytes + lane * 128;
+                for (int c = 0; c < halves * 8; ++c)
+                    *reinterpret_cast<uint4*>(row + (c >> 3) * kHalfBytes + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                fence_proxy_async_shared();  // before the ring's next load of these bytes
+            }
+            __syncwarp();
         }
         {
-            const int r = (lane & 7) + ((lane >> 4) << 3), hi = (lane >> 3) & 1;
+            const uint32_t base =
+                smem_u32(ring) + stage * unit_bytes + ((lane & 7) + ((lane >> 4) << 3)) * 128;
+            const int r7 = lane & 7, hi = (lane >> 3) & 1;
 #pragma unroll
             for (int mt = 0; mt < kSlice / 16; ++mt) {
                 if (mt * 16 >= width) break;
-                uint32_t vf[4];
-                ldsm4_t(vs + r * kRowBytes + (((2 * mt + hi) ^ (r & 7)) << 4), vf);
+                const uint32_t at = base + (mt >> 2) * kHalfBytes + (((2 * (mt & 3) + hi) ^ r7) << 4);
+                uint32_t va[4], vb[4];
+                ldsm4_t(at, va);
+                ldsm4_t(at + 16 * 128, vb);
                 o[mt][0] *= f0c;
                 o[mt][1] *= f1c;
                 o[mt][2] *= f0c;
                 o[mt][3] *= f1c;
-                mma_bf16(o[mt], vf, ph[0], ph[1]);
-                mma_bf16(o[mt], vf, pl[0], pl[1]);
+                mma_bf16(o[mt], va, ph[0][0], ph[0][1]);
+                mma_bf16(o[mt], vb, ph[1][0], ph[1][1]);
+                mma_bf16(o[mt], va, pl[0][0], pl[0][1]);
+                mma_bf16(o[mt], vb, pl[1][0], pl[1][1]);
             }
         }
-        __syncwarp();  // the ring's stage has been read
+        unit_done();
         const bool ends = cur.s + 1 == cur.sp.s1;
         if (ends || step + 1 == g1) {
             // ---- a piece, or a whole item, is done
@@ -390,7 +437,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_attention_kernel(Deco
             }
             const bool whole = begins && ends;
             const float r0 = whole ? (t0 > 0.f ? 1.f / t0 : 0.f) : 1.f, r1 = whole ? (t1 > 0.f ? 1.f / t1 : 0.f) : 1.f;
-            const int dp = a.tw * a.slice;
+            const int dp = a.tw * kSlice;
             float* part = a.part + (size_t)(my_team * 2 + (begins ? 1 : 0)) * piece_floats(8, dp);
 #pragma unroll
             for (int mt = 0; mt < kSlice / 16; ++mt) {
@@ -432,7 +479,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) cache_attention_kernel(Deco
             open = false;
         }
         if (step + 1 < g1) cur.next(a);
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    if (dead) {
+        // leave no copy in flight (each wait is bounded again)
+        for (int i = 0; i < n_units; ++i) {
+            mbar_wait(&s_full[warp][stage], phase, kErrTimeoutLoad);
+            if (++stage == n_units) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
     }
 }
 
@@ -447,7 +503,7 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(DecodeArgs a) 
     if (head >= min(8, a.group - hblk * 8)) return;
     __shared__ float s_m[kJoinThreads / 32], s_l[kJoinThreads / 32];
     __shared__ float4 s_o[kJoinThreads];
-    const int dp = a.tw * a.slice, lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    const int dp = a.tw * kSlice, lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const size_t pf = piece_floats(8, dp);
     const int t0 = blockIdx.x, n = job.z - t0 + 1;  // pieces: (t0, starts), (t0 + 1, goes on), ...
     auto piece = [&](int i) { return a.part + ((size_t)(t0 + i) * 2 + (i == 0 ? 1 : 0)) * pf; };
