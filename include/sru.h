@@ -438,8 +438,8 @@ sru_status sru_cache_extend(const int32_t* lengths, const int32_t* new_tokens, i
  * caches, rounded to bf16.  A negative slot writes nothing; one >= pages *
  * page_size writes nothing and is reported as SRU_ERR_INVALID by the next
  * sru_sync_status().  Of two rows with the same slot either may win, element by
- * element.  Limits: D % 8 == 0; k_ld, v_ld multiples of 16 bytes; K, V and the
- * caches 16-byte aligned.
+ * element.  Limits: D % 8 == 0; k_ld, v_ld multiples of 16 bytes; T * Hkv * D below
+ * 2^35; K, V and the caches 16-byte aligned.
  */
 sru_status sru_cache_append(const void* K, int64_t k_ld, const void* V, int64_t v_ld, int t, const int32_t* slots,
                             void* k_cache, void* v_cache, int64_t T, int64_t Hkv, int64_t D, int64_t page_size,

@@ -13,7 +13,6 @@ element-wise recurrence), with a highway scale alpha.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -388,20 +387,54 @@ def sru_decode_step(X_t, W, x_t, v, b, c, h_t, alpha: float = 1.0, workspace=Non
     return h_t, c
 
 
-def _same_device(*tensors):
-    """Context that makes the tensors' device current for a launch; raises unless they share one CUDA device."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1 or next(iter(devices)).type != "cuda":
-        raise ValueError("tensors must live on one CUDA device")
-    index = next(iter(devices)).index
-    return contextlib.nullcontext() if index == torch.cuda.current_device() else torch.cuda.device(index)
+# The loss and cache calls below check and pass their tensors through these: a decoding step calls several of
+# them per layer on sizes where the kernels take a few microseconds, so the host's part is kept as short.
+def _device_of(*tensors) -> int:
+    """Index of the CUDA device that all the tensors (None skipped) live on; raises otherwise."""
+    index = None
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d != index:
+                if index is not None or d < 0:
+                    raise ValueError("tensors must live on one CUDA device")
+                index = d
+    return index
 
 
-def _scratch(nbytes: int, device, stream) -> Optional[torch.Tensor]:
+def _data(t: Optional[torch.Tensor], dtype) -> Optional[int]:
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"expected {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    return t.data_ptr()
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(fn, device: int, stream, *args):
+    """fn(*args, stream) with the tensors' device current, on `stream` or that device's current stream."""
+    if stream is not None:
+        handle = stream.cuda_stream
+    else:
+        handle = _raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device:
+        status = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, handle)
+    if status != SRU_OK:
+        raise SRUError(status, fn.__name__, _lib)
+
+
+def _scratch(nbytes: int, device: int, stream) -> Optional[torch.Tensor]:
     """A workspace for one call: torch reuses it only after the call's stream has passed it."""
     if nbytes == 0:
         return None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
     if stream is not None and stream != torch.cuda.current_stream(device):
         ws.record_stream(stream)
     return ws
@@ -414,8 +447,8 @@ def sru_softmax_loss_workspace_bytes(M: int, V: int, K: int, backward: bool = Tr
 
 def _loss_shapes(H, W, targets, *rows):
     M, K = H.shape
-    V = W.shape[0]
-    if tuple(W.shape) != (V, K) or tuple(targets.shape) != (M,) or any(tuple(t.shape) != (M,) for t in rows):
+    V, Kw = W.shape
+    if Kw != K or targets.shape != (M,) or any(t.shape != (M,) for t in rows):
         raise ValueError("shape mismatch")
     return M, V, K
 
@@ -428,12 +461,12 @@ def sru_softmax_loss(H, W, targets, loss, lse, workspace=None, stream=None):
     bytes is allocated when none is given."""
     lib = load_library()
     M, V, K = _loss_shapes(H, W, targets, loss, lse)
-    with _same_device(H, W, targets, loss, lse, workspace):
-        if workspace is None:
-            workspace = _scratch(sru_softmax_loss_workspace_bytes(M, V, K, False), H.device, stream)
-        _check(lib.sru_softmax_loss(_ptr(H, torch.bfloat16), _ptr(W, torch.bfloat16), _ptr(targets, torch.int64),
-                                    _ptr(loss, torch.float32), _ptr(lse, torch.float32), M, V, K, _ptr(workspace),
-                                    _nbytes(workspace), _stream(stream)), "sru_softmax_loss")
+    dev = _device_of(H, W, targets, loss, lse, workspace)
+    if workspace is None:
+        workspace = _scratch(sru_softmax_loss_workspace_bytes(M, V, K, False), dev, stream)
+    _call(lib.sru_softmax_loss, dev, stream, _data(H, torch.bfloat16), _data(W, torch.bfloat16),
+          _data(targets, torch.int64), _data(loss, torch.float32), _data(lse, torch.float32), M, V, K,
+          *_bytes(workspace))
     return loss, lse
 
 
@@ -445,17 +478,26 @@ def sru_softmax_loss_backward(H, W, targets, lse, dloss, dH=None, dW=None, works
     none is given."""
     lib = load_library()
     M, V, K = _loss_shapes(H, W, targets, lse, dloss)
-    if (dH is not None and tuple(dH.shape) != (M, K)) or (dW is not None and tuple(dW.shape) != (V, K)):
+    if (dH is not None and dH.shape != (M, K)) or (dW is not None and dW.shape != (V, K)):
         raise ValueError("gradient shape mismatch")
-    with _same_device(H, W, targets, lse, dloss, dH, dW, workspace):
-        if workspace is None:
-            workspace = _scratch(sru_softmax_loss_workspace_bytes(M, V, K, True), H.device, stream)
-        _check(lib.sru_softmax_loss_backward(
-            _ptr(H, torch.bfloat16), _ptr(W, torch.bfloat16), _ptr(targets, torch.int64), _ptr(lse, torch.float32),
-            _ptr(dloss, torch.float32), _ptr(dH), SRU_F32 if dH is None else _dtype_code(dH), _ptr(dW),
-            SRU_F32 if dW is None else _dtype_code(dW), M, V, K, _ptr(workspace), _nbytes(workspace),
-            _stream(stream)), "sru_softmax_loss_backward")
+    dev = _device_of(H, W, targets, lse, dloss, dH, dW, workspace)
+    if workspace is None:
+        workspace = _scratch(sru_softmax_loss_workspace_bytes(M, V, K, True), dev, stream)
+    h_t, w_t = (SRU_F32 if t is None else _dtype_code(t) for t in (dH, dW))
+    _call(lib.sru_softmax_loss_backward, dev, stream, _data(H, torch.bfloat16), _data(W, torch.bfloat16),
+          _data(targets, torch.int64), _data(lse, torch.float32), _data(dloss, torch.float32),
+          _data(dH, dH.dtype if dH is not None else None), h_t, _data(dW, dW.dtype if dW is not None else None), w_t,
+          M, V, K, *_bytes(workspace))
     return dH, dW
+
+
+def _bytes(workspace: Optional[torch.Tensor]):
+    """Pointer and size of a workspace."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        raise ValueError("tensor must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def sru_cache_extend(lengths, new_tokens, block_table, free_pages, free_count, page_size: int, lengths_out,
@@ -470,28 +512,26 @@ def sru_cache_extend(lengths, new_tokens, block_table, free_pages, free_count, p
     may be lengths and free_count."""
     lib = load_library()
     B, maxp = block_table.shape
-    one = [free_count, free_count_out] + ([] if refused is None else [refused])
-    if any(tuple(t.shape) != (B,) for t in (lengths, new_tokens, lengths_out)) or any(t.numel() != 1 for t in one) \
-            or offsets.numel() != B + 1 or free_pages.dim() != 1 or slots.dim() != 1:
+    if not lengths.shape == new_tokens.shape == lengths_out.shape == (B,) or offsets.shape != (B + 1,) \
+            or free_count.numel() != 1 or free_count_out.numel() != 1 or free_pages.dim() != 1 or slots.dim() != 1 \
+            or (refused is not None and refused.numel() != 1):
         raise ValueError("shape mismatch")
+    dev = _device_of(lengths, new_tokens, block_table, free_pages, free_count, lengths_out, free_count_out, offsets,
+                     slots, refused)
     i32 = torch.int32
-    with _same_device(lengths, new_tokens, block_table, free_pages, free_count, lengths_out, free_count_out, offsets,
-                      slots, refused):
-        _check(lib.sru_cache_extend(_ptr(lengths, i32), _ptr(new_tokens, i32), _ptr(block_table, i32),
-                                    _ptr(free_pages, i32), _ptr(free_count, i32), B, maxp, free_pages.numel(),
-                                    page_size, slots.numel(), _ptr(lengths_out, i32), _ptr(free_count_out, i32),
-                                    _ptr(offsets, i32), _ptr(slots, i32), _ptr(refused, i32), _stream(stream)),
-               "sru_cache_extend")
+    _call(lib.sru_cache_extend, dev, stream, _data(lengths, i32), _data(new_tokens, i32), _data(block_table, i32),
+          _data(free_pages, i32), _data(free_count, i32), B, maxp, free_pages.numel(), page_size, slots.numel(),
+          _data(lengths_out, i32), _data(free_count_out, i32), _data(offsets, i32), _data(slots, i32),
+          _data(refused, i32))
     return lengths_out, offsets, slots
 
 
 def _row_strided(t: torch.Tensor, H: int, D: int):
     """Pointer and row pitch of (T, H, D) rows that are packed within a row."""
-    if not t.is_cuda:
-        raise ValueError("tensor must live on a CUDA device")
-    if t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D)):
+    ld, sh, sd = t.stride()
+    if t.numel() and (sd != 1 or (H > 1 and sh != D)):
         raise ValueError("the heads of a row must be contiguous")
-    return ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else H * D
+    return t.data_ptr(), ld if t.shape[0] > 1 else H * D
 
 
 def sru_cache_append(K, V, slots, k_cache, v_cache, stream=None):
@@ -499,16 +539,14 @@ def sru_cache_append(K, V, slots, k_cache, v_cache, stream=None):
     (pages, Hkv, page_size, D) bf16; a negative slot writes nothing.  K and V may be
     views of a wider matrix (rows any multiple of 16 bytes apart)."""
     lib = load_library()
-    T, H, D = K.shape
+    T, H, D = shape = K.shape
     pages, Hc, ps, Dc = k_cache.shape
-    if K.shape != V.shape or K.dtype != V.dtype or (Hc, Dc) != (H, D) or k_cache.shape != v_cache.shape \
-            or tuple(slots.shape) != (T,):
+    if V.shape != shape or K.dtype != V.dtype or Hc != H or Dc != D or k_cache.shape != v_cache.shape \
+            or slots.shape != (T,):
         raise ValueError("shape mismatch")
-    with _same_device(K, V, slots, k_cache, v_cache):
-        (kp, k_ld), (vp, v_ld) = _row_strided(K, H, D), _row_strided(V, H, D)
-        _check(lib.sru_cache_append(kp, k_ld, vp, v_ld, _dtype_code(K), _ptr(slots, torch.int32),
-                                    _ptr(k_cache, torch.bfloat16), _ptr(v_cache, torch.bfloat16), T, H, D, ps, pages,
-                                    _stream(stream)), "sru_cache_append")
+    dev = _device_of(K, V, slots, k_cache, v_cache)
+    _call(lib.sru_cache_append, dev, stream, *_row_strided(K, H, D), *_row_strided(V, H, D), _dtype_code(K),
+          _data(slots, torch.int32), _data(k_cache, torch.bfloat16), _data(v_cache, torch.bfloat16), T, H, D, ps, pages)
     return k_cache, v_cache
 
 
@@ -528,19 +566,17 @@ def sru_attention_decode(q, k_cache, v_cache, block_table, lengths, out, scale: 
     lib = load_library()
     B, Hq, D = q.shape
     pages, Hkv, ps, Dc = k_cache.shape
-    if Dc != D or k_cache.shape != v_cache.shape or out.shape != q.shape or block_table.dim() != 2 \
-            or block_table.shape[0] != B or tuple(lengths.shape) != (B,) \
-            or (lse is not None and tuple(lse.shape) != (B, Hq)):
+    Bt, maxp = block_table.shape
+    if Dc != D or k_cache.shape != v_cache.shape or out.shape != q.shape or Bt != B or lengths.shape != (B,) \
+            or (lse is not None and lse.shape != (B, Hq)):
         raise ValueError("shape mismatch")
-    with _same_device(q, k_cache, v_cache, block_table, lengths, out, lse, workspace):
-        if workspace is None:
-            workspace = _scratch(sru_attention_decode_workspace_bytes(B, Hq, Hkv, D), q.device, stream)
-        _check(lib.sru_attention_decode(_ptr(q, torch.bfloat16), _ptr(k_cache, torch.bfloat16),
-                                        _ptr(v_cache, torch.bfloat16), _ptr(block_table, torch.int32),
-                                        _ptr(lengths, torch.int32), _ptr(out), _dtype_code(out),
-                                        _ptr(lse, torch.float32), B, Hq, Hkv, D, ps, pages, block_table.shape[1],
-                                        window, D ** -0.5 if scale is None else float(scale), _ptr(workspace),
-                                        _nbytes(workspace), _stream(stream)), "sru_attention_decode")
+    dev = _device_of(q, k_cache, v_cache, block_table, lengths, out, lse, workspace)
+    if workspace is None:
+        workspace = _scratch(sru_attention_decode_workspace_bytes(B, Hq, Hkv, D), dev, stream)
+    _call(lib.sru_attention_decode, dev, stream, _data(q, torch.bfloat16), _data(k_cache, torch.bfloat16),
+          _data(v_cache, torch.bfloat16), _data(block_table, torch.int32), _data(lengths, torch.int32),
+          _data(out, out.dtype), _dtype_code(out), _data(lse, torch.float32), B, Hq, Hkv, D, ps, pages, maxp, window,
+          D ** -0.5 if scale is None else scale, *_bytes(workspace))
     return out
 
 

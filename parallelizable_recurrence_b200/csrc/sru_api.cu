@@ -1938,7 +1938,27 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
     return SRU_OK;
 }
 
+}  // extern "C"
+
 // ---- paged key/value cache and the attention of one new token over it
+// A kernel that starts with pdl_wait: its launch overlaps the kernel before it.
+template <typename Args>
+static sru_status launch_dependent(void (*kern)(Args), dim3 grid, unsigned threads, cudaStream_t st, const Args& a) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    SRU_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, a));
+    return SRU_OK;
+}
+
+extern "C" {
+
 static sru_status check_cache_sizes(int64_t pages, int64_t ps) {
     if (pages < 0 || ps < 1) return SRU_ERR_INVALID;
     if (pages >= ((int64_t)1 << 31) || ps >= ((int64_t)1 << 31) || pages * ps >= ((int64_t)1 << 31))
@@ -1947,8 +1967,9 @@ static sru_status check_cache_sizes(int64_t pages, int64_t ps) {
 }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// New rows above which the step's bookkeeping runs on a cluster of 8 CTAs.
-constexpr int64_t kExtendClusterRows = 8192;
+// Rows from which a second kernel writes the slots (one CTA writes about 1000 rows a
+// microsecond next to its sums; the second launch costs about 3).
+constexpr int64_t kExtendRowsKernel = 4096;
 
 sru_status sru_cache_extend(const int32_t* lengths, const int32_t* new_tokens, int32_t* table, int32_t* free_pages,
                             const int32_t* free_count, int64_t B, int64_t max_pages, int64_t pages, int64_t page_size,
@@ -1968,20 +1989,15 @@ sru_status sru_cache_extend(const int32_t* lengths, const int32_t* new_tokens, i
         if (!aligned4(p)) return SRU_ERR_INVALID;
     sru::cache::ExtendArgs a{lengths,     new_tokens,     table,   free_pages, free_count, lengths_out,
                              free_count_out, offsets,     slots,   refused,    (int)B,     (int)max_pages,
-                             (int)pages,  (int)page_size, (int)T};
-    const unsigned ctas = T > kExtendClusterRows ? 8 : 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(sru::cache::kExtThreads);
-    cfg.stream = as_stream(stream);
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = ctas;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    SRU_CUDA_TRY(cudaLaunchKernelEx(&cfg, sru::cache::cache_extend_kernel, a));
-    return SRU_OK;
+                             (int)pages,  (int)page_size, (int)T,  T > kExtendRowsKernel};
+    const unsigned threads = (unsigned)std::min<int64_t>(std::max<int64_t>((B + 31) / 32 * 32, 64),
+                                                         sru::cache::kExtThreads);
+    cudaStream_t st = as_stream(stream);
+    sru::cache::cache_extend_kernel<<<1, threads, 0, st>>>(a);
+    SRU_CUDA_TRY(cudaGetLastError());
+    if (!a.rows_kernel) return SRU_OK;
+    const int64_t rows = 8 * sru::cache::kSlotRows;
+    return launch_dependent(sru::cache::cache_slots_kernel, dim3((unsigned)((T + rows - 1) / rows)), 256, st, a);
 }
 
 sru_status sru_cache_append(const void* K, int64_t k_ld, const void* V, int64_t v_ld, int t, const int32_t* slots,
@@ -2000,19 +2016,18 @@ sru_status sru_cache_append(const void* K, int64_t k_ld, const void* V, int64_t 
     if (!K || !V || !slots || !aligned16(K) || !aligned16(V) || !aligned4(slots)) return SRU_ERR_INVALID;
     if (pages > 0 && (!k_cache || !v_cache)) return SRU_ERR_INVALID;
     if (!aligned16(k_cache) || !aligned16(v_cache)) return SRU_ERR_INVALID;
-    const size_t items = (size_t)T * (Hkv * D / 8);
-    const dim3 grid((unsigned)std::min<size_t>(blocks_for(std::min<size_t>(items, (size_t)1 << 38), 256),
-                                               (size_t)sm_count() * 32),
-                    2);
+    const int64_t items = T * (Hkv * D / 8);
+    if (items >= (int64_t)1 << 32) return SRU_ERR_UNSUPPORTED;
+    const dim3 grid(blocks_for((size_t)items, 256 * sru::cache::kAppendItems), 2);
     __nv_bfloat16 *kc = static_cast<__nv_bfloat16*>(k_cache), *vc = static_cast<__nv_bfloat16*>(v_cache);
     if (t == SRU_BF16)
         sru::cache::cache_append_kernel<<<grid, 256, 0, as_stream(stream)>>>(
             static_cast<const __nv_bfloat16*>(K), (long long)k_ld, static_cast<const __nv_bfloat16*>(V),
-            (long long)v_ld, slots, kc, vc, (int)T, (int)Hkv, (int)D, (int)page_size, (long long)(pages * page_size));
+            (long long)v_ld, slots, kc, vc, (unsigned)items, (int)Hkv, (int)D, (int)page_size, (long long)(pages * page_size));
     else
         sru::cache::cache_append_kernel<<<grid, 256, 0, as_stream(stream)>>>(
             static_cast<const float*>(K), (long long)k_ld, static_cast<const float*>(V), (long long)v_ld, slots, kc,
-            vc, (int)T, (int)Hkv, (int)D, (int)page_size, (long long)(pages * page_size));
+            vc, (unsigned)items, (int)Hkv, (int)D, (int)page_size, (long long)(pages * page_size));
     SRU_CUDA_TRY(cudaGetLastError());
     return SRU_OK;
 }
@@ -2103,10 +2118,9 @@ sru_status sru_attention_decode(const void* q, const void* k_cache, const void* 
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((steps + p.teams - 1) / p.teams, sm_count()));
     sru::cache::cache_attention_kernel<<<(unsigned)grid, threads, smem, st>>>(mk, mv, a);
     SRU_CUDA_TRY(cudaGetLastError());
-    const dim3 jgrid((unsigned)(grid * p.teams), (unsigned)std::min<int64_t>(8, Hq / Hkv), (unsigned)((D + 127) / 128));
-    sru::cache::cache_join_kernel<<<jgrid, sru::cache::kJoinThreads, 0, st>>>(a);
-    SRU_CUDA_TRY(cudaGetLastError());
-    return SRU_OK;
+    return launch_dependent(sru::cache::cache_join_kernel,
+                            dim3((unsigned)grid, (unsigned)std::min<int64_t>(8, Hq / Hkv), (unsigned)((D + 127) / 128)),
+                            sru::cache::kJoinWarps * 32, st, a);
 }
 
 sru_status sru_sync_status(void* stream) {

@@ -22,15 +22,14 @@ namespace cache {
 //   pages come off its top, as long as the running sum of the needs stays within
 //   the stack's height (and the tokens within the table's width and the step's
 //   rows), else the request is refused and keeps what it had.
-// Three running sums (new tokens, released pages, needed pages) over the
-// requests, then independent writes.  The call is bound by latency: one launch
-// of one CTA, or of one cluster of 8 when there are many slots to write; every
-// CTA computes the sums of all requests (8 bytes each), which costs less than
-// passing them on, and the cluster's barrier orders pushes before pops and
-// reads before in-place writes.
+// Two passes over the requests, a thread each: running sums of the new tokens and
+// of the released pages, then of the needs.  The call is bound by latency, so one
+// CTA, no wider than the requests need, does the sums and everything that a
+// request's own thread or warp can write.  A step with room for many rows gets a
+// second kernel over the rows for the requests of more than kExtDirect tokens; it
+// learns from such a request's first slot, written here, whether it was refused.
 constexpr int kExtThreads = 1024;
-constexpr int kExtDirect = 8;   // tokens that a request's own thread writes; more are shared out in segments
-constexpr int kExtSeg = 256;    // tokens per segment (one warp)
+constexpr int kExtDirect = 4;  // tokens that a request's own thread writes
 
 struct ExtendArgs {
     const int *lengths, *add;
@@ -38,158 +37,191 @@ struct ExtendArgs {
     const int* n_free;
     int *lengths_out, *n_free_out, *offsets, *slots, *refused;
     int B, maxp, pages, ps, T;
+    int rows_kernel;  // long runs of slots are left to cache_slots_kernel
 };
 
-template <typename T>
-__device__ __forceinline__ T warp_inclusive(T v, int lane) {
+// Inclusive sum over the block's threads; `total` gets the whole sum.
+__device__ __forceinline__ unsigned long long warp_inclusive(unsigned long long v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const T u = __shfl_up_sync(0xffffffffu, v, o);
+        const unsigned long long u = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += u;
     }
     return v;
 }
-// Inclusive sum over the block's threads; `total` gets the whole sum.
-template <typename T>
-__device__ __forceinline__ T block_inclusive(T v, T* warp_sums, T& total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ unsigned long long block_inclusive(unsigned long long v, unsigned long long* warp_sums,
+                                                              unsigned long long& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
     v = warp_inclusive(v, lane);
-    __syncthreads();  // warp_sums may still be read from the last use
     if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
-    const T w = warp_inclusive(lane < kExtThreads / 32 ? warp_sums[lane] : T(0), lane);
+    const unsigned long long w = warp_inclusive(lane < n_warps ? warp_sums[lane] : 0ull, lane);
     total = __shfl_sync(0xffffffffu, w, 31);
-    const T before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
-    return v + (warp == 0 ? T(0) : before);
+    const unsigned long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    __syncthreads();  // warp_sums may be written again
+    return v + (warp == 0 ? 0ull : before);
 }
 
 __global__ void __launch_bounds__(kExtThreads) cache_extend_kernel(ExtendArgs a) {
-    __shared__ long long sums[kExtThreads / 32];
-    // this chunk's requests, for the segments
-    __shared__ int s_seg[kExtThreads], s_first[kExtThreads], s_len[kExtThreads], s_held[kExtThreads],
-        s_top[kExtThreads], s_add[kExtThreads];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t rank = 0, ncta = gridDim.x;
-    if (ncta > 1) rank = cluster_ctarank();
+    __shared__ unsigned long long sums[kExtThreads / 32];
+    __shared__ int s_refused, s_taken;
+    const int tid = threadIdx.x, lane = tid & 31, nt = blockDim.x;
+    pdl_launch();
+    if (tid == 0) s_refused = s_taken = 0;
     const long long width = (long long)a.maxp * a.ps;
     const int n_free = max(0, min(*a.n_free, a.pages));
 
-    auto read = [&](int b, int& len, int& add, int& held) {
+    int len = 0, add = 0, held = 0;
+    auto read = [&](int b) {
         len = b < a.B ? max(a.lengths[b], 0) : 0;
         add = b < a.B ? a.add[b] : 0;
-        held = (int)min((long long)(len / a.ps) + (len % a.ps != 0), (long long)a.maxp);
+        held = min((int)(((long long)len + a.ps - 1) / a.ps), a.maxp);
     };
-    // a page of the stack once the released pages lie on it
-    auto stack = [&](long long i) { return i >= 0 && i < a.pages ? a.free_pages[i] : -1; };
+    // an entry of the stack once the released pages lie on it
+    auto stack = [&](int i) { return i >= 0 && i < a.pages ? a.free_pages[i] : -1; };
 
-    // ---- released pages onto the stack
-    long long gone_before = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kExtThreads) {
-        int len, add, held;
-        read(b0 + tid, len, add, held);
+    // ---- released pages onto the stack; sums: new tokens (low word), released pages (high)
+    unsigned long long upto = 0, total = 0;
+    int gone_before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += nt) {
+        read(b0 + tid);
         const int gone = add < 0 ? held : 0;
-        long long total;
-        const long long upto = block_inclusive<long long>(gone, sums, total);
-        const long long base = n_free + gone_before + upto - gone;
-        if ((uint32_t)warp % ncta == rank) {
-            for (unsigned left = __ballot_sync(0xffffffffu, gone > 0); left != 0; left &= left - 1) {
-                const int src = __ffs(left) - 1;
-                const int n = __shfl_sync(0xffffffffu, gone, src);
-                const long long at = __shfl_sync(0xffffffffu, base, src);
-                const int* row = a.table + (size_t)(b0 + warp * 32 + src) * a.maxp;
-                for (int i = lane; i < n; i += 32)
-                    if (at + i < a.pages) a.free_pages[at + i] = row[i];
-            }
+        upto = block_inclusive((unsigned)max(add, 0) | (unsigned long long)gone << 32, sums, total);
+        const int base = n_free + gone_before + (int)(upto >> 32) - gone;
+        for (unsigned left = __ballot_sync(0xffffffffu, gone > 0); left != 0; left &= left - 1) {
+            const int src = __ffs(left) - 1;
+            const int n = __shfl_sync(0xffffffffu, gone, src), at = __shfl_sync(0xffffffffu, base, src);
+            const int* row = a.table + (size_t)(b0 + tid - lane + src) * a.maxp;
+            for (int i = lane; i < n; i += 32)
+                if (at + i >= 0 && at + i < a.pages) a.free_pages[at + i] = row[i];
         }
-        gone_before += total;
+        gone_before += (int)(total >> 32);
     }
-    if (ncta > 1) cluster_sync_all();
-    else __syncthreads();
-    const long long avail = min(n_free + gone_before, (long long)a.pages);
+    __syncthreads();
+    const int avail = min(n_free + gone_before, a.pages);
 
-    // ---- grants, slots and lengths
-    long long first_before = 0, need_before = 0, taken = 0;
-    int refused = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kExtThreads) {
+    // ---- grants, table entries, slots and lengths
+    unsigned first_before = 0;
+    int need_before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += nt) {
         const int b = b0 + tid;
-        int len, add, held;
-        read(b, len, add, held);
-        const int grow = max(add, 0);
-        if (ncta > 1) cluster_sync_all();  // every CTA has read this chunk: it may be written in place
-        long long total;
-        const long long last = first_before + block_inclusive<long long>(grow, sums, total);
-        first_before += total;
-        const long long first = last - grow, end = (long long)len + grow;
-        const bool fits = grow > 0 && end <= width && last <= a.T;
-        const int need = fits ? (int)((end + a.ps - 1) / a.ps) - held : 0;
-        const long long upto = need_before + block_inclusive<long long>(need, sums, total);
-        need_before += total;
-        const bool ok = fits && (need == 0 || upto <= avail);
-        const int take = ok ? need : 0;
-        block_inclusive<long long>(take, sums, total);
-        taken += total;
-        refused += __syncthreads_count(grow > 0 && !ok);
-        // page index i >= held of this request is stack entry top - i
-        const int top = (int)(avail - 1 - (upto - need)) + held;
-        const bool direct = grow <= kExtDirect;
-        const int seg = direct ? 0 : (int)((min((long long)grow, max(0ll, a.T - first)) + kExtSeg - 1) / kExtSeg);
-        long long segs;
-        const long long seg_upto = block_inclusive<long long>(seg, sums, segs);
-        s_seg[tid] = (int)seg_upto;
-        s_first[tid] = (int)min(first, (long long)a.T);
-        s_len[tid] = len;
-        s_held[tid] = held;
-        s_top[tid] = top;
-        s_add[tid] = ok ? grow : -grow;  // negative: refused
-        auto token = [&](int bb, int j, int len_, int held_, int top_, bool ok_, long long at) {
-            int slot = -1;
-            if (ok_) {
-                const int pos = len_ + j, p = pos / a.ps, in = pos - p * a.ps;
-                const int page = p < held_ ? a.table[(size_t)bb * a.maxp + p] : stack(top_ - p);
-                if (p >= held_ && in == 0) a.table[(size_t)bb * a.maxp + p] = page;  // its first token is new
-                if (page >= 0) slot = page * a.ps + in;
-            }
-            if (at < a.T) a.slots[at] = slot;
-        };
-        if (direct && (uint32_t)warp % ncta == rank)
-            for (int j = 0; j < grow; ++j) token(b, j, len, held, top, ok, first + j);
-        __syncthreads();
-        for (long long q = (long long)rank * (kExtThreads / 32) + warp; q < segs;
-             q += (long long)ncta * (kExtThreads / 32)) {
-            int lo = 0, hi = kExtThreads - 1;  // the first request whose running segment count passes q
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (s_seg[mid] > q) hi = mid;
-                else lo = mid + 1;
-            }
-            const int j0 = (int)(q - (lo == 0 ? 0 : s_seg[lo - 1])) * kExtSeg;
-            const int n = abs(s_add[lo]);
-#pragma unroll
-            for (int k = 0; k < kExtSeg; k += 32)
-                if (j0 + k + lane < n)
-                    token(b0 + lo, j0 + k + lane, s_len[lo], s_held[lo], s_top[lo], s_add[lo] > 0,
-                          (long long)s_first[lo] + j0 + k + lane);
+        if (a.B > nt) {  // (one chunk: its values are still at hand)
+            read(b);
+            upto = block_inclusive((unsigned)max(add, 0), sums, total);
         }
-        if (rank == 0 && b < a.B) {
+        const int grow = max(add, 0);
+        const unsigned last = first_before + (unsigned)upto, first = last - grow;
+        first_before += (unsigned)total;
+        const long long end = (long long)len + grow;
+        const bool fits = grow > 0 && end <= width && last <= (unsigned)a.T;
+        const int need = fits ? (int)((end + a.ps - 1) / a.ps) - held : 0;
+        const int wanted = need_before + (int)block_inclusive((unsigned)need, sums, total);
+        need_before += (int)total;
+        const bool ok = fits && (need == 0 || wanted <= avail);
+        const int refused = __popc(__ballot_sync(0xffffffffu, grow > 0 && !ok));
+        const int taken = __reduce_max_sync(0xffffffffu, ok && need > 0 ? wanted : 0);  // grants are a prefix of the needs
+        if (lane == 0) {
+            if (refused) atomicAdd(&s_refused, refused);
+            if (taken) atomicMax(&s_taken, taken);
+        }
+        // page p >= held of this request is stack entry top - p
+        const int top = avail - 1 - (wanted - need) + held, take = ok ? need : 0;
+        int* row = a.table + (size_t)b * a.maxp;
+        if (take <= 2) {
+            for (int i = 0; i < take; ++i) row[held + i] = stack(top - held - i);
+        }
+        for (unsigned left = __ballot_sync(0xffffffffu, take > 2); left != 0; left &= left - 1) {
+            const int src = __ffs(left) - 1;
+            const int n = __shfl_sync(0xffffffffu, take, src), at = __shfl_sync(0xffffffffu, held, src);
+            const int from = __shfl_sync(0xffffffffu, top, src);
+            int* r = a.table + (size_t)(b0 + tid - lane + src) * a.maxp;
+            for (int i = at + lane; i < at + n; i += 32) r[i] = stack(from - i);
+        }
+        // slot of token j of a request
+        auto slot = [&](const int* r, int len_, int held_, int top_, int j) {
+            const int pos = len_ + j, p = pos / a.ps;
+            const int page = p < held_ ? r[p] : stack(top_ - p);
+            return page < 0 ? -1 : page * a.ps + (pos - p * a.ps);
+        };
+        // (a refused request's rows may reach behind T; `first` below T is below 2^31)
+        if (grow > 0 && first < (unsigned)a.T) {
+            const int n = grow <= kExtDirect ? grow : (a.rows_kernel ? 1 : 0);
+            for (int j = 0; j < n; ++j)
+                if (first + j < (unsigned)a.T) a.slots[first + j] = ok ? slot(row, len, held, top, j) : -1;
+        }
+        if (!a.rows_kernel) {
+            for (unsigned left = __ballot_sync(0xffffffffu, grow > kExtDirect && first < (unsigned)a.T); left != 0;
+                 left &= left - 1) {
+                const int src = __ffs(left) - 1;
+                const int n = __shfl_sync(0xffffffffu, grow, src), at = __shfl_sync(0xffffffffu, (int)first, src);
+                const int len_ = __shfl_sync(0xffffffffu, len, src), held_ = __shfl_sync(0xffffffffu, held, src);
+                const int top_ = __shfl_sync(0xffffffffu, top, src);
+                const bool ok_ = __shfl_sync(0xffffffffu, (int)ok, src) != 0;
+                const int* r = a.table + (size_t)(b0 + tid - lane + src) * a.maxp;
+                const int rows = min(n, a.T - at);
+                for (int j = lane; j < rows; j += 32) a.slots[at + j] = ok_ ? slot(r, len_, held_, top_, j) : -1;
+            }
+        }
+        if (b < a.B) {
             a.lengths_out[b] = add < 0 ? 0 : (ok ? (int)end : len);
             a.offsets[b] = (int)first;
         }
-        __syncthreads();
     }
-    // rows behind the last token
-    for (long long i = first_before + (long long)rank * kExtThreads + tid; i < a.T; i += (long long)ncta * kExtThreads)
-        a.slots[i] = -1;
-    if (rank == 0 && tid == 0) {
+    __syncthreads();
+    if (!a.rows_kernel)  // rows behind the last token
+        for (unsigned i = first_before + tid; i < (unsigned)a.T; i += nt) a.slots[i] = -1;
+    if (tid == 0) {
         a.offsets[a.B] = (int)first_before;
-        *a.n_free_out = (int)(avail - taken);
-        if (a.refused != nullptr) *a.refused = refused;
+        *a.n_free_out = avail - s_taken;
+        if (a.refused != nullptr) *a.refused = s_refused;
+    }
+}
+
+// The slots that cache_extend_kernel leaves: rows of requests with more than
+// kExtDirect tokens (all but the first row) and the rows behind the last token.  A
+// warp takes kSlotRows consecutive rows, finds the request of its first one by
+// a 33-way search of the offsets and walks on from there.
+constexpr int kSlotRows = 128;
+__global__ void __launch_bounds__(256) cache_slots_kernel(ExtendArgs a) {
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const long long t0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kSlotRows;
+    if (t0 >= a.T) return;
+    const int total = a.offsets[a.B];
+    int lo = 0, hi = a.B;  // offsets[lo] <= t0 < offsets[hi], if t0 < total
+    while (hi - lo > 1) {
+        const int probe = lo + (int)((long long)(hi - lo) * (lane + 1) / 33);
+        const int n = __popc(__ballot_sync(0xffffffffu, a.offsets[probe] <= t0));  // (probe = lo counts)
+        const int new_lo = n == 0 ? lo : lo + (int)((long long)(hi - lo) * n / 33);
+        if (n < 32) hi = lo + (int)((long long)(hi - lo) * (n + 1) / 33);
+        lo = new_lo;
+    }
+    int b = lo;
+#pragma unroll
+    for (int i = 0; i < kSlotRows; i += 32) {
+        const int t = (int)t0 + i + lane;
+        if (t >= a.T) return;
+        if (t >= total) {
+            a.slots[t] = -1;
+            continue;
+        }
+        while (a.offsets[b + 1] <= t) ++b;
+        const int first = a.offsets[b], n = a.offsets[b + 1] - first;
+        if (n <= kExtDirect || t == first) continue;
+        int s = -1;
+        if (a.slots[first] >= 0) {
+            const int pos = a.lengths_out[b] - n + (t - first), p = pos / a.ps;
+            const int page = a.table[(size_t)b * a.maxp + p];
+            if (page >= 0) s = page * a.ps + (pos - p * a.ps);
+        }
+        a.slots[t] = s;
     }
 }
 
 // -------------------------------------------------------------------------- append
 // Row r of K and V (T rows of Hkv * D elements, k_ld / v_ld apart) to slot
 // slots[r] of the caches, rounded to bf16; a negative slot writes nothing.  Pure
-// copy: 16-byte stores, one per thread and item.
+// copy, bound by memory: 16-byte items, four in flight per thread.
 template <typename SrcT>
 __device__ __forceinline__ uint4 load8_bf16(const SrcT* p) {
     if (sizeof(SrcT) == 2) return __ldg(reinterpret_cast<const uint4*>(p));
@@ -198,27 +230,42 @@ __device__ __forceinline__ uint4 load8_bf16(const SrcT* p) {
                            __floats2bfloat162_rn(b.x, b.y), __floats2bfloat162_rn(b.z, b.w)};
     return *reinterpret_cast<uint4*>(w);
 }
+constexpr int kAppendItems = 4;  // 16-byte stores per thread, their loads issued together
 template <typename SrcT>
 __global__ void __launch_bounds__(256)
     cache_append_kernel(const SrcT* __restrict__ K, long long k_ld, const SrcT* __restrict__ V, long long v_ld,
                         const int* __restrict__ slots, __nv_bfloat16* __restrict__ k_cache,
-                        __nv_bfloat16* __restrict__ v_cache, int T, int Hkv, int D, int ps, long long n_slots) {
+                        __nv_bfloat16* __restrict__ v_cache, unsigned items, int Hkv, int D, int ps,
+                        long long n_slots) {
     const SrcT* src = blockIdx.y == 0 ? K : V;
     const long long ld = blockIdx.y == 0 ? k_ld : v_ld;
     __nv_bfloat16* dst = blockIdx.y == 0 ? k_cache : v_cache;
-    const int vd = D / 8, per_row = Hkv * vd;
-    const long long n = (long long)T * per_row;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
-        const int r = (int)(i / per_row), c = (int)(i - (long long)r * per_row);
-        const int slot = slots[r];
-        if (slot < 0) continue;
-        if (slot >= n_slots) {
+    const unsigned vd = D / 8, per_row = Hkv * vd;
+    const unsigned i0 = blockIdx.x * (256u * kAppendItems) + threadIdx.x;
+    uint4 v[kAppendItems];
+    int slot[kAppendItems];
+    unsigned col[kAppendItems];
+#pragma unroll
+    for (int k = 0; k < kAppendItems; ++k) {
+        const unsigned i = i0 + k * 256u;
+        slot[k] = -1;
+        if (i < items && i >= i0) {
+            const unsigned r = i / per_row;
+            col[k] = i - r * per_row;
+            slot[k] = __ldg(slots + r);
+            v[k] = load8_bf16(src + r * ld + (long long)col[k] * 8);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kAppendItems; ++k) {
+        if (slot[k] < 0) continue;
+        if (slot[k] >= n_slots) {
             record_error(kErrBadIndex);
             continue;
         }
-        const int h = c / vd, page = slot / ps;
-        const size_t at = (((size_t)page * Hkv + h) * ps + (slot - page * ps)) * D + (size_t)(c - h * vd) * 8;
-        *reinterpret_cast<uint4*>(dst + at) = load8_bf16(src + r * ld + (long long)c * 8);
+        const unsigned h = col[k] / vd, page = (unsigned)slot[k] / ps;
+        const size_t at = (((size_t)page * Hkv + h) * ps + (slot[k] - page * ps)) * D + (size_t)(col[k] - h * vd) * 8;
+        *reinterpret_cast<uint4*>(dst + at) = v[k];
     }
 }
 

@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthreads = blockDim.x;
     const int HH = a.Hkv * a.blocks;
 
+    pdl_launch();
     if (lane == 0) {
         for (int i = 0; i < kMaxUnits; ++i) mbar_init(&s_full[warp][i], 1);
         fence_mbar_init();
@@ -492,72 +493,103 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     }
 }
 
-// Joins the pieces of one item and head: grid (teams, heads of a block, feature
-// slices of 128), 8 groups of 32 threads x 4 features that take pieces in turn.
-// The order of the sums is fixed by the sizes alone.
-constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(DecodeArgs a) {
-    const int4 job = a.jobs[blockIdx.x];
-    if (job.x < 0) return;
-    const int head = blockIdx.y, hblk = job.y % a.blocks, kv = job.y / a.blocks;
-    if (head >= min(8, a.group - hblk * 8)) return;
-    __shared__ float s_m[kJoinThreads / 32], s_l[kJoinThreads / 32];
-    __shared__ float4 s_o[kJoinThreads];
-    const int dp = a.tw * kSlice, lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+// Joins the pieces of the items that the teams of main CTA blockIdx.x start, for one
+// head (blockIdx.y) and 128 features (blockIdx.z; a lane has 4).  An item of up to
+// 8 pieces is joined by the warp of its team; a longer one by all warps, which
+// take pieces in turn.  The order of the sums is fixed by the sizes alone.
+constexpr int kJoinWarps = kMaxWarps;
+__global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(DecodeArgs a) {
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
+    __shared__ float4 s_o[kJoinWarps][32];
+    pdl_wait();
+    const int dp = a.tw * kSlice, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const size_t pf = piece_floats(8, dp);
-    const int t0 = blockIdx.x, n = job.z - t0 + 1;  // pieces: (t0, starts), (t0 + 1, goes on), ...
-    auto piece = [&](int i) { return a.part + ((size_t)(t0 + i) * 2 + (i == 0 ? 1 : 0)) * pf; };
-    float top = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += kJoinThreads) top = fmaxf(top, piece(i)[(size_t)8 * dp + head]);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    if (lane == 0) s_m[grp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kJoinThreads / 32; ++i) top = fmaxf(top, s_m[i]);
-    const float base = top == -INFINITY ? 0.f : top;
-    const int c = blockIdx.z * 128 + lane * 4;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int i = grp; i < n; i += kJoinThreads / 32) {
-        const float* p = piece(i);
-        const float w = ex2f(p[(size_t)8 * dp + head] - base);
-        l = __fmaf_rn(w, p[(size_t)8 * dp + 8 + head], l);
-        if (c < a.D) {
-            const float4 x = *reinterpret_cast<const float4*>(p + (size_t)head * dp + c);
-            acc.x = __fmaf_rn(w, x.x, acc.x);
-            acc.y = __fmaf_rn(w, x.y, acc.y);
-            acc.z = __fmaf_rn(w, x.z, acc.z);
-            acc.w = __fmaf_rn(w, x.w, acc.w);
+    const int head = blockIdx.y, c = blockIdx.z * 128 + lane * 4;
+    const bool live = c < a.D;
+
+    auto store = [&](const int4& job, float4 acc, float top, float l) {
+        const float r = l > 0.f ? 1.f / l : 0.f;
+        const int hblk = job.y % a.blocks, kv = job.y / a.blocks;
+        const size_t row = (size_t)job.x * a.Hq + kv * a.group + hblk * 8 + head;
+        if (live) {
+            if (a.out_f32)
+                *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * a.D + c) =
+                    make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
+            else
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * a.D + c) =
+                    make_uint2(pack_bf16(acc.x * r, acc.y * r), pack_bf16(acc.z * r, acc.w * r));
         }
-    }
-    s_o[threadIdx.x] = acc;
-    if (lane == 0) s_l[grp] = l;
-    __syncthreads();
-    if (grp != 0) return;
-    l = 0.f;
+        if (a.lse != nullptr && blockIdx.z == 0 && lane == 0)
+            a.lse[row] = l > 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    };
+    auto add = [](float4& acc, float w, const float4& x) {
+        acc.x = __fmaf_rn(w, x.x, acc.x);
+        acc.y = __fmaf_rn(w, x.y, acc.y);
+        acc.z = __fmaf_rn(w, x.z, acc.z);
+        acc.w = __fmaf_rn(w, x.w, acc.w);
+    };
+
+    for (int t = 0; t < a.teams; ++t) {
+        const int t0 = blockIdx.x * a.teams + t;
+        const int4 job = a.jobs[t0];
+        if (job.x < 0 || head >= min(8, a.group - job.y % a.blocks * 8)) continue;
+        const int n = job.z - t0 + 1;  // pieces: (t0, starts), (t0 + 1, goes on), ...
+        auto piece = [&](int i) { return a.part + ((size_t)(t0 + i) * 2 + (i == 0 ? 1 : 0)) * pf; };
+        if (n <= kJoinWarps) {
+            if (warp != t) continue;
+            const float m = lane < n ? piece(lane)[(size_t)8 * dp + head] : -INFINITY;
+            const float li = lane < n ? piece(lane)[(size_t)8 * dp + 8 + head] : 0.f;
+            float4 x[kJoinWarps];
 #pragma unroll
-    for (int i = 0; i < kJoinThreads / 32; ++i) l += s_l[i];
-    for (int i = 1; i < kJoinThreads / 32; ++i) {
-        const float4 x = s_o[i * 32 + lane];
-        acc.x += x.x;
-        acc.y += x.y;
-        acc.z += x.z;
-        acc.w += x.w;
+            for (int i = 0; i < kJoinWarps; ++i)
+                if (i < n && live) x[i] = *reinterpret_cast<const float4*>(piece(i) + (size_t)head * dp + c);
+            float top = m;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            top = __shfl_sync(0xffffffffu, top, 0);
+            const float w = ex2f(m - (top == -INFINITY ? 0.f : top));
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f;
+#pragma unroll
+            for (int i = 0; i < kJoinWarps; ++i) {
+                if (i >= n) break;
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                l = __fmaf_rn(wi, __shfl_sync(0xffffffffu, li, i), l);
+                if (live) add(acc, wi, x[i]);
+            }
+            store(job, acc, top, l);
+            continue;
+        }
+        float top = -INFINITY;
+        for (int i = threadIdx.x; i < n; i += kJoinWarps * 32) top = fmaxf(top, piece(i)[(size_t)8 * dp + head]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0) s_m[warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, s_m[i]);
+        const float base = top == -INFINITY ? 0.f : top;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+#pragma unroll 8
+        for (int i = warp; i < n; i += kJoinWarps) {
+            const float* p = piece(i);
+            const float w = ex2f(p[(size_t)8 * dp + head] - base);
+            l = __fmaf_rn(w, p[(size_t)8 * dp + 8 + head], l);
+            if (live) add(acc, w, *reinterpret_cast<const float4*>(p + (size_t)head * dp + c));
+        }
+        s_o[warp][lane] = acc;
+        if (lane == 0) s_l[warp] = l;
+        __syncthreads();
+        if (warp == 0) {
+            for (int i = 1; i < kJoinWarps; ++i) {
+                add(acc, 1.f, s_o[i][lane]);
+                l += s_l[i];
+            }
+            store(job, acc, top, l);
+        }
+        __syncthreads();  // the shared sums may be written again
     }
-    const float r = l > 0.f ? 1.f / l : 0.f;
-    const size_t row = (size_t)job.x * a.Hq + kv * a.group + hblk * 8 + head;
-    if (c < a.D) {
-        if (a.out_f32)
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * a.D + c) =
-                make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
-        else
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * a.D + c) =
-                make_uint2(pack_bf16(acc.x * r, acc.y * r), pack_bf16(acc.z * r, acc.w * r));
-    }
-    if (a.lse != nullptr && blockIdx.z == 0 && lane == 0)
-        a.lse[row] = l > 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace cache

@@ -244,4 +244,11 @@ __device__ __forceinline__ void tc_commit_pair_mc(uint64_t* bar, uint16_t cta_ma
         : "memory");
 }
 
+
+// ---- programmatic dependent launch: the next kernel on the stream, if launched
+// so, may begin its prologue once every CTA of this one has called pdl_launch (or
+// left); its pdl_wait returns when this kernel has completed and its writes are visible.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 }  // namespace sru
