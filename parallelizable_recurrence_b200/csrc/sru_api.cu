@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <chrono>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -1941,19 +1943,22 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
 }  // extern "C"
 
 // ---- paged key/value cache and the attention of one new token over it
-// A kernel that starts with pdl_wait: its launch overlaps the kernel before it.
-template <typename Args>
-static sru_status launch_dependent(void (*kern)(Args), dim3 grid, unsigned threads, cudaStream_t st, const Args& a) {
+// Launch of a kernel that calls pdl_wait before it touches memory: it may start while the
+// kernel before it on the stream runs out.
+template <typename... Params, typename... Args>
+static sru_status launch_overlapped(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
+                                    const Args&... args) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    SRU_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, a));
+    SRU_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, args...));
     return SRU_OK;
 }
 
@@ -1993,11 +1998,10 @@ sru_status sru_cache_extend(const int32_t* lengths, const int32_t* new_tokens, i
     const unsigned threads = (unsigned)std::min<int64_t>(std::max<int64_t>((B + 31) / 32 * 32, 64),
                                                          sru::cache::kExtThreads);
     cudaStream_t st = as_stream(stream);
-    sru::cache::cache_extend_kernel<<<1, threads, 0, st>>>(a);
-    SRU_CUDA_TRY(cudaGetLastError());
-    if (!a.rows_kernel) return SRU_OK;
+    s = launch_overlapped(sru::cache::cache_extend_kernel, dim3(1), threads, 0, st, a);
+    if (s != SRU_OK || !a.rows_kernel) return s;
     const int64_t rows = 8 * sru::cache::kSlotRows;
-    return launch_dependent(sru::cache::cache_slots_kernel, dim3((unsigned)((T + rows - 1) / rows)), 256, st, a);
+    return launch_overlapped(sru::cache::cache_slots_kernel, dim3((unsigned)((T + rows - 1) / rows)), 256, 0, st, a);
 }
 
 sru_status sru_cache_append(const void* K, int64_t k_ld, const void* V, int64_t v_ld, int t, const int32_t* slots,
@@ -2021,31 +2025,39 @@ sru_status sru_cache_append(const void* K, int64_t k_ld, const void* V, int64_t 
     const dim3 grid(blocks_for((size_t)items, 256 * sru::cache::kAppendItems), 2);
     __nv_bfloat16 *kc = static_cast<__nv_bfloat16*>(k_cache), *vc = static_cast<__nv_bfloat16*>(v_cache);
     if (t == SRU_BF16)
-        sru::cache::cache_append_kernel<<<grid, 256, 0, as_stream(stream)>>>(
-            static_cast<const __nv_bfloat16*>(K), (long long)k_ld, static_cast<const __nv_bfloat16*>(V),
-            (long long)v_ld, slots, kc, vc, (unsigned)items, (int)Hkv, (int)D, (int)page_size, (long long)(pages * page_size));
-    else
-        sru::cache::cache_append_kernel<<<grid, 256, 0, as_stream(stream)>>>(
-            static_cast<const float*>(K), (long long)k_ld, static_cast<const float*>(V), (long long)v_ld, slots, kc,
-            vc, (unsigned)items, (int)Hkv, (int)D, (int)page_size, (long long)(pages * page_size));
-    SRU_CUDA_TRY(cudaGetLastError());
-    return SRU_OK;
+        return launch_overlapped(sru::cache::cache_append_kernel<__nv_bfloat16>, grid, 256, 0, as_stream(stream),
+                                 static_cast<const __nv_bfloat16*>(K), (long long)k_ld,
+                                 static_cast<const __nv_bfloat16*>(V), (long long)v_ld, slots, kc, vc, (unsigned)items,
+                                 (int)Hkv, (int)D, (int)page_size, (long long)(pages * page_size));
+    return launch_overlapped(sru::cache::cache_append_kernel<float>, grid, 256, 0, as_stream(stream),
+                             static_cast<const float*>(K), (long long)k_ld, static_cast<const float*>(V),
+                             (long long)v_ld, slots, kc, vc, (unsigned)items, (int)Hkv, (int)D, (int)page_size,
+                             (long long)(pages * page_size));
 }
 
 constexpr int64_t kDecodeMaxD = (int64_t)sru::cache::kSlice * sru::cache::kMaxWarps;
 struct DecodePlan {
     int tw, teams, blocks;
-    size_t jobs_off, total;
+    size_t flags_off, total;
 };
 static DecodePlan decode_plan(int64_t Hq, int64_t Hkv, int64_t D) {
     DecodePlan p{};
     p.tw = (int)((D + sru::cache::kSlice - 1) / sru::cache::kSlice);
     p.teams = sru::cache::kMaxWarps / p.tw;
     p.blocks = (int)((Hq / Hkv + 7) / 8);
-    const size_t teams = (size_t)sm_count() * p.teams;
-    p.jobs_off = round256(teams * 2 * sru::cache::piece_floats(8, p.tw * sru::cache::kSlice) * sizeof(float));
-    p.total = p.jobs_off + round256(teams * sizeof(int4));
+    // two pieces per CTA, a slice per warp for pieces that end early
+    const size_t ctas = (size_t)sm_count();
+    p.flags_off = round256((ctas * 2 * sru::cache::piece_floats(p.tw) +
+                            ctas * sru::cache::kMaxWarps * sru::cache::kSliceFloats) * sizeof(float));
+    p.total = p.flags_off + round256(ctas * 2 * sizeof(unsigned long long));
     return p;
+}
+// A number of its own for every call (47 bits, from a start that the clock scatters):
+// it tells this call's flags from whatever else lies in the workspace.
+static unsigned long long next_tag() {
+    static std::atomic<unsigned long long> tag{(unsigned long long)
+        std::chrono::system_clock::now().time_since_epoch().count() * 0x9e3779b97f4a7c15ull};
+    return (tag.fetch_add(1) & 0x7fffffffffffull) | 1ull << 47;
 }
 static sru_status check_decode_sizes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D) {
     if (B < 0 || Hq < 1 || Hkv < 1 || D < 1 || Hq % Hkv != 0) return SRU_ERR_INVALID;
@@ -2085,7 +2097,8 @@ sru_status sru_attention_decode(const void* q, const void* k_cache, const void* 
     a.out = out;
     a.lse = lse;
     a.part = reinterpret_cast<float*>(ws);
-    a.jobs = reinterpret_cast<int4*>(ws + p.jobs_off);
+    a.flags = reinterpret_cast<unsigned long long*>(ws + p.flags_off);
+    a.tag = next_tag();
     a.B = (int)B; a.Hq = (int)Hq; a.Hkv = (int)Hkv; a.D = (int)D;
     if (pages == 0) max_pages = 0;  // no key can be read
     a.ps = (int)page_size; a.maxp = (int)max_pages; a.pages = (int)pages;
@@ -2097,30 +2110,44 @@ sru_status sru_attention_decode(const void* q, const void* k_cache, const void* 
     a.scale_log2 = scale * 1.4426950408889634f;
     cudaStream_t st = as_stream(stream);
     const int threads = p.tw * p.teams * 32;
-    const size_t smem = (size_t)p.tw * p.teams * sru::cache::kRingBytes + 1024;
-    SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(sru::cache::cache_attention_kernel),
-                             (size_t)sru::cache::kMaxWarps * sru::cache::kRingBytes + 1024));
-    // the caches as (D, page_size, pages * Hkv), in boxes of 64 features x box_rows rows of
-    // one page; without pages nothing is loaded through them
+    // the rings, and room for the pieces that end early where it is left (the static part is
+    // the scores' exchange, which a team of one warp does not have)
+    const size_t rings = (size_t)p.tw * p.teams * sru::cache::kRingBytes + 1024;
+    const size_t early = (size_t)p.tw * p.teams * std::min<int64_t>(8, a.group) * sru::cache::kSlice * sizeof(float);
+    const size_t most = (size_t)(D == 128 ? 225 : 208) * 1024;
+    const bool fits = rings + early <= most;
+    const size_t smem = rings + (fits ? early : 0);
+    a.early_floats = fits ? (int)(early / sizeof(float)) / (p.tw * p.teams) : 0;
+    // D = 128, 256, 512, 1024: the forms without loops over the width
+    auto kern = D == 128   ? sru::cache::cache_attention_kernel<1>
+                : D == 256 ? sru::cache::cache_attention_kernel<2>
+                : D == 512 ? sru::cache::cache_attention_kernel<4>
+                : D == 1024 ? sru::cache::cache_attention_kernel<8>
+                            : sru::cache::cache_attention_kernel<0>;
+    SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kern), most));
+    // a wide team's pieces cost more to join than a few more steps of one team
+    a.min_steps = std::max(1, p.tw / 2);
+    // The caches as (D, page_size, pages * Hkv), in boxes of 64 features x box_rows rows of
+    // one page; for D a multiple of 64 as (64, page_size, D / 64, pages * Hkv), so that one
+    // box holds a warp's 128 features.  Without pages nothing is loaded through the maps.
     CUtensorMap mk{}, mv{};
+    a.merged = D % 64 == 0;
     if (pages > 0) {
-        const uint64_t dims[3] = {(uint64_t)D, (uint64_t)page_size, (uint64_t)(pages * Hkv)};
-        const uint64_t strides[2] = {(uint64_t)D * 2, (uint64_t)(page_size * D) * 2};
-        const uint32_t box[3] = {64, (uint32_t)a.box_rows, 1};
-        if (!make_map(&mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, k_cache, dims, strides, box,
-                      CU_TENSOR_MAP_SWIZZLE_128B) ||
-            !make_map(&mv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, v_cache, dims, strides, box,
-                      CU_TENSOR_MAP_SWIZZLE_128B))
-            return SRU_ERR_INVALID;
+        const uint64_t row = (uint64_t)D * 2, page = (uint64_t)(page_size * D) * 2, heads = (uint64_t)(pages * Hkv);
+        const uint64_t dims3[3] = {(uint64_t)D, (uint64_t)page_size, heads}, strides3[2] = {row, page};
+        const uint64_t dims4[4] = {64, (uint64_t)page_size, (uint64_t)D / 64, heads}, strides4[3] = {row, 128, page};
+        const uint32_t box3[3] = {64, (uint32_t)a.box_rows, 1};
+        const uint32_t box4[4] = {64, (uint32_t)a.box_rows, D > 64 ? 2u : 1u, 1};
+        for (int i = 0; i < 2; ++i)
+            if (!make_map(i ? &mv : &mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.merged ? 4 : 3, i ? v_cache : k_cache,
+                          a.merged ? dims4 : dims3, a.merged ? strides4 : strides3, a.merged ? box4 : box3,
+                          CU_TENSOR_MAP_SWIZZLE_128B))
+                return SRU_ERR_INVALID;
     }
     // no more teams than there can be steps
     const int64_t steps = B * Hkv * p.blocks * ((max_pages * page_size + sru::cache::kStep - 1) / sru::cache::kStep);
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((steps + p.teams - 1) / p.teams, sm_count()));
-    sru::cache::cache_attention_kernel<<<(unsigned)grid, threads, smem, st>>>(mk, mv, a);
-    SRU_CUDA_TRY(cudaGetLastError());
-    return launch_dependent(sru::cache::cache_join_kernel,
-                            dim3((unsigned)grid, (unsigned)std::min<int64_t>(8, Hq / Hkv), (unsigned)((D + 127) / 128)),
-                            sru::cache::kJoinWarps * 32, st, a);
+    return launch_overlapped(kern, dim3((unsigned)grid), threads, smem, st, mk, mv, a);
 }
 
 sru_status sru_sync_status(void* stream) {

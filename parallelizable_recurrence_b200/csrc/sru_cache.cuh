@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kExtThreads) cache_extend_kernel(ExtendArgs a)
     __shared__ int s_refused, s_taken;
     const int tid = threadIdx.x, lane = tid & 31, nt = blockDim.x;
     pdl_launch();
+    pdl_wait();
     if (tid == 0) s_refused = s_taken = 0;
     const long long width = (long long)a.maxp * a.ps;
     const int n_free = max(0, min(*a.n_free, a.pages));
@@ -183,6 +184,7 @@ __global__ void __launch_bounds__(kExtThreads) cache_extend_kernel(ExtendArgs a)
 // a 33-way search of the offsets and walks on from there.
 constexpr int kSlotRows = 128;
 __global__ void __launch_bounds__(256) cache_slots_kernel(ExtendArgs a) {
+    pdl_launch();
     pdl_wait();
     const int lane = threadIdx.x & 31;
     const long long t0 = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * kSlotRows;
@@ -237,6 +239,8 @@ __global__ void __launch_bounds__(256)
                         const int* __restrict__ slots, __nv_bfloat16* __restrict__ k_cache,
                         __nv_bfloat16* __restrict__ v_cache, unsigned items, int Hkv, int D, int ps,
                         long long n_slots) {
+    pdl_launch();
+    pdl_wait();
     const SrcT* src = blockIdx.y == 0 ? K : V;
     const long long ld = blockIdx.y == 0 ? k_ld : v_ld;
     __nv_bfloat16* dst = blockIdx.y == 0 ? k_cache : v_cache;

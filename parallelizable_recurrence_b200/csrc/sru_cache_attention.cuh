@@ -8,23 +8,26 @@
 // and value is read once and used for 2 x (heads of its group) multiplications:
 // the call is bound by reading the cache.
 //
-// One pass with a running maximum m and sum l per head.  A step is 16 keys.  The
+// One pass with a running maximum m and sum l per head.  A step is 32 keys.  The
 // steps of all (request, key head) items form one list, cut in equal contiguous
 // ranges, one per team, so that ragged lengths still load every SM alike; a
 // team's loads run ahead of its products across item borders.  An item that
-// spans teams leaves its pieces (m, l, unnormalised o, fp32) in the workspace
-// and cache_join_kernel joins them.
+// spans teams is in pieces (m, l, unnormalised o, fp32): the teams of a CTA join
+// theirs through shared memory, and of the CTAs that share an item the last to
+// finish joins theirs through the workspace, in the order of the keys whoever that
+// is.  (A second kernel for it cost 5 to 9 us.)
 //
 // A team is TW = ceil(D / 128) warps; warp w owns features 128 w .. of q, k, v and
-// o.  It loads its part itself, by TMA: units of 32 rows x 128 features, K and V in
-// turn, through a ring of its own whose barriers no other warp touches.  A page
-// of ps tokens allows boxes of R rows, R the largest power of two (<= 32) that
-// divides ps.  Keys are rows of the tensor-core products -- S^T = K Q^T (16 keys x
-// 8 heads), O^T = V^T P^T (16 features x 8 heads) -- so a group of up to 8 heads
-// costs what one does, and only the 32 x 8 partial scores cross the team's warps,
-// through shared memory.  p enters its product as two bf16 parts (value and
-// remainder, 16 bits together), so o is as exact as fp32 scores make it; the second
-// product is free next to the loads.
+// o.  It loads its part itself, by TMA: units of 32 rows x 128 features through a
+// ring of three whose barriers no other warp touches.  A page of ps tokens allows
+// boxes of R rows, R the largest power of two (<= 32) that divides ps.  Keys are
+// rows of the tensor-core products -- S^T = K Q^T (16 keys x 8 heads), O^T = V^T P^T
+// (16 features x 8 heads) -- so a group of up to 8 heads costs what one does, and
+// only the 32 x 8 partial scores cross the team's warps, through shared memory.  The
+// scores of step i + 1 are taken before the values of step i, so that neither the
+// exchange nor the products' latency is waited for.  p enters its product as two
+// bf16 parts (value and remainder, 16 bits together), so o is as exact as fp32
+// scores make it; the second product is free next to the loads.
 #pragma once
 
 #include "sru_ptx.cuh"
@@ -37,25 +40,30 @@ constexpr int kSlice = 128;   // features per warp
 constexpr int kMaxWarps = 8;  // per CTA
 constexpr uint32_t kHalfBytes = kStep * 128;       // 64 features of a step's rows
 constexpr uint32_t kRingBytes = 6 * kHalfBytes;    // per warp: 3 units, or 6 of one half when D <= 64
-constexpr int kMaxUnits = 6, kMasks = 4;
+constexpr int kMasks = 4;     // steps whose keys' mask is held
 
 struct DecodeArgs {
     const __nv_bfloat16 *q, *k, *v;
     const int *table, *lengths;
     void* out;
-    float* lse;          // nullable
-    float* part;         // pieces: team * 2 + (1 = starts its item, 0 = goes on with it)
-    int4* jobs;          // per team: the item that it starts and does not finish
+    float* lse;                  // nullable
+    float* part;                 // pieces: (CTA, goes on with / starts its item), then the teams' first ones
+    unsigned long long* flags;   // the same index: the CTA's piece is there, if equal to
+    unsigned long long tag;      // this call's number
     int B, Hq, Hkv, D, ps, maxp, pages, window, out_f32;
     int group;           // query heads per key head
     int blocks;          // head blocks per key head
     int tw, teams;       // warps per team, teams per CTA
     int box_rows;        // R
+    int merged;          // the maps are 4-D and one box holds both halves of a unit's rows
+    int min_steps;       // per team
+    int early_floats;    // shared floats per warp for a piece that ends before its team's range; 0: workspace
     float scale_log2;    // scale * log2 e
 };
 
-// floats of one piece: o [heads][tw * kSlice], then m and l [heads]
-__host__ __device__ inline size_t piece_floats(int heads, int dp) { return (size_t)heads * dp + 2 * heads; }
+// A piece: o [tw][8 heads][kSlice], then m and l [8].
+constexpr int kSliceFloats = 8 * kSlice;
+__host__ __device__ inline size_t piece_floats(int tw) { return (size_t)tw * kSliceFloats + 16; }
 
 __device__ __forceinline__ float ex2f(float x) {
     float y;
@@ -126,28 +134,46 @@ struct Cursor {
     }
 };
 
+// A run of pieces of one item, found from the CTA's (or the CTAs') bookkeeping.
+struct Item {
+    int b, hh;
+    long long first, last;  // its steps in the list
+};
+
+// TW = 0: any number of warps per team and any width; otherwise TW warps of 128 features
+// each (D = 128 TW), which makes the loops over features and warps straight code.
+template <int TW>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     cache_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                           DecodeArgs a) {
+                           const __grid_constant__ DecodeArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ float4 exch[2][kMaxWarps][2][32];
+    constexpr int kMaxUnits = TW > 0 ? 3 : 6;
     __shared__ uint64_t s_full[kMaxWarps][kMaxUnits];
     __shared__ uint32_t s_mask[kMaxWarps][kMasks];
     __shared__ long long s_scan[kMaxWarps], s_rem[kMaxWarps];
     __shared__ int s_b[kMaxWarps];
+    // pieces of each team: [0] goes on with an item (1: and not to its end, 2: to its end), [1] starts one
+    __shared__ int s_has[kMaxWarps][2], s_end[kMaxWarps];  // s_end: [0] is the range's last step
+    __shared__ Item s_item[kMaxWarps][2];
+    __shared__ float s_ml[kMaxWarps][2][16];   // their m and l
+    __shared__ int s_last[2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthreads = blockDim.x;
     const int HH = a.Hkv * a.blocks;
+    const int tw = TW > 0 ? TW : a.tw, teams = TW > 0 ? kMaxWarps / TW : a.teams;
 
-    pdl_launch();
     if (lane == 0) {
         for (int i = 0; i < kMaxUnits; ++i) mbar_init(&s_full[warp][i], 1);
         fence_mbar_init();
+        s_has[warp][0] = s_has[warp][1] = 0;
     }
     if (tid == 0) {
         tma_prefetch_desc(&map_k);
         tma_prefetch_desc(&map_v);
     }
+    pdl_launch();
+    pdl_wait();
     // ---- this CTA's teams' places in the list: sums of steps over the requests
     const int per_thread = (a.B + nthreads - 1) / nthreads;
     long long mine = 0;
@@ -168,10 +194,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
     }
-    const long long n_teams = (long long)gridDim.x * a.teams;
-    const long long per = max(1ll, (total + n_teams - 1) / n_teams);
-    for (int t = 0; t < a.teams; ++t) {
-        const long long g0 = ((long long)blockIdx.x * a.teams + t) * per;
+    const long long n_teams = (long long)gridDim.x * teams;
+    const long long per = max((long long)a.min_steps, (total + n_teams - 1) / n_teams);
+    for (int t = 0; t < teams; ++t) {
+        const long long g0 = ((long long)blockIdx.x * teams + t) * per;
         if (g0 >= before && g0 < before + mine) {
             long long at = before;
             for (int b = tid * per_thread;; ++b) {
@@ -185,28 +211,22 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             }
         }
     }
-    // requests without keys: their output is zero
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const Span sp = span_of(a, b);
-        if (tid == 0 && a.lengths[b] > sp.hi) record_error(kErrBadIndex);  // longer than the table is wide
-        if (sp.steps() > 0) continue;
-        for (int i = tid; i < a.Hq * a.D; i += nthreads) {
-            const size_t at = (size_t)b * a.Hq * a.D + i;
-            if (a.out_f32) static_cast<float*>(a.out)[at] = 0.f;
-            else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(0.f);
-        }
-        if (a.lse != nullptr)
-            for (int i = tid; i < a.Hq; i += nthreads) a.lse[(size_t)b * a.Hq + i] = -INFINITY;
-    }
     __syncthreads();
 
-    const int team = warp / a.tw, w_in = warp - team * a.tw;
-    const long long my_team = (long long)blockIdx.x * a.teams + team;
+    auto heads_of = [&](int hh) { return min(8, a.group - hh % a.blocks * 8); };
+    auto head0_of = [&](int hh) { return hh / a.blocks * a.group + hh % a.blocks * 8; };
+    const int team = warp / tw, w_in = warp - team * tw;
+    const long long my_team = (long long)blockIdx.x * teams + team;
     const long long g0 = my_team * per, g1 = min(total, g0 + per);
-    if (g0 >= g1) {
-        if (w_in == 0 && lane == 0) a.jobs[my_team] = make_int4(-1, 0, 0, 0);
-        return;
-    }
+    const int n_steps = g0 < g1 ? (int)(g1 - g0) : 0;
+
+    uint8_t* ring = smem + warp * kRingBytes;
+    // a piece that ends within the range: behind the rings, or in the workspace
+    float* early = a.early_floats > 0
+                       ? reinterpret_cast<float*>(smem + tw * teams * kRingBytes) + (size_t)warp * a.early_floats
+                       : a.part + (size_t)gridDim.x * 2 * piece_floats(tw) +
+                             ((size_t)blockIdx.x * kMaxWarps + warp) * kSliceFloats;
+    if (n_steps > 0) {
     Cursor cur;
     {
         cur.b = s_b[team];
@@ -215,79 +235,90 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         cur.hh = (int)(s_rem[team] / n);
         cur.s = cur.sp.s0 + (int)(s_rem[team] - (long long)cur.hh * n);
     }
-    Cursor ld = cur;
+    const int f0 = w_in * kSlice;                                   // first feature of this warp
+    const int width = TW > 0 ? kSlice : min(kSlice, a.D - f0);      // its features, a multiple of 8
+    const int n_units = TW > 0 || a.D > 64 ? 3 : 6, halves = TW > 0 || a.D > 64 ? 2 : 1;
+    const uint32_t unit_bytes = halves * kHalfBytes;
 
-    const int f0 = w_in * kSlice;                   // first feature of this warp
-    const int width = min(kSlice, a.D - f0);        // its features, a multiple of 8
-    const int halves = width > 64 ? 2 : 1;          // boxes of 64 features
-    const int n_units = a.D > 64 ? 3 : 6;
-    const uint32_t unit_bytes = a.D > 64 ? 2 * kHalfBytes : kHalfBytes;
-    uint8_t* ring = smem + warp * kRingBytes;
+    // ---- loads.  Lane l has the box of row group l; units come in the order of use: K of step
+    // 0, then K of step j + 1 and V of step j, at last V of the last step.
     const int R = a.box_rows, groups = kStep / R;
-    const int my_group = lane & (groups - 1), my_half = lane / groups;  // boxes of this lane: my_half, + 32 / groups
-
-    // Table entry of this lane's box of step `ld`: read one step before its load, so
-    // that its latency is not waited for.
-    int next_page = 0, next_in = -1;  // next_in < 0: no key of the box is wanted
-    auto fetch_page = [&]() {
-        const int pos = ld.s * kStep + my_group * R;
+    const int boxes = a.merged ? 1 : (width > 64 ? 2 : 1);          // per group
+    const uint32_t box_bytes = R * 128 * (a.merged ? halves : 1);
+    Cursor ld = cur;
+    int next_page = 0, next_in = -1;  // table entry of this lane's box of step `ld`; < 0: no key of it is wanted
+    auto fetch_page = [&]() {         // (read one step before its load, so that its latency is not waited for)
+        const int pos = ld.s * kStep + lane * R;
         next_in = -1;
-        if (pos + R > ld.sp.lo && pos < ld.sp.hi) {
+        if (lane < groups && pos + R > ld.sp.lo && pos < ld.sp.hi) {
             const int p = pos / a.ps;
             next_page = __ldg(a.table + (size_t)ld.b * a.maxp + p);
             next_in = pos - p * a.ps;
         }
     };
-    int box_row = 0, box_in = -1;  // this lane's box of the step being loaded
-    uint32_t step_bytes = 0;
-    long long loaded = g0;         // step of the next unit to load
-    int load_unit = 0, load_stage = 0, mask_at = 0;  // load_unit: 0 = K, 1 = V
-    bool dead = false;             // a wait ran out: no further loads or waits
+    int k_row = 0, k_in = -1, v_row = 0, v_in = -1;  // this lane's box of the step whose K (V) is loaded
+    uint32_t k_bytes = 0, v_bytes = 0;
+    int k_next = 0, v_next = 0, load_stage = 0;      // steps whose K and V come next
+    bool dead = false;                               // a wait ran out: no further loads or waits
     auto load_next = [&]() {
-        if (loaded >= g1 || dead) return;
-        uint64_t* bar = &s_full[warp][load_stage];
-        uint8_t* dst = ring + load_stage * unit_bytes;
-        if (load_unit == 0) {
-            box_in = next_in;
-            if (box_in >= 0 && (unsigned)next_page >= (unsigned)a.pages) {
+        if (v_next >= n_steps || dead) return;
+        const bool is_k = k_next < n_steps && k_next <= v_next + 1;
+        if (is_k || v_next + 1 == k_next) {  // (the last V has no K after it)
+            v_row = k_row;
+            v_in = k_in;
+            v_bytes = k_bytes;
+        }
+        if (is_k) {
+            k_in = next_in;
+            if (k_in >= 0 && (unsigned)next_page >= (unsigned)a.pages) {
                 record_error(kErrBadIndex);  // its keys are left out
-                box_in = -1;
+                k_in = -1;
             }
-            box_row = (int)((unsigned)next_page * a.Hkv + ld.hh / a.blocks);
-            const unsigned there = __ballot_sync(0xffffffffu, box_in >= 0) & (groups == 32 ? ~0u : (1u << groups) - 1);
-            step_bytes = __popc(there) * halves * R * 128;
+            k_row = (int)((unsigned)next_page * a.Hkv + ld.hh / a.blocks);
+            const unsigned there = __ballot_sync(0xffffffffu, k_in >= 0);
+            k_bytes = __popc(there) * boxes * box_bytes;
             const int pos = ld.s * kStep + lane;
             const unsigned mask =
                 __ballot_sync(0xffffffffu, pos >= ld.sp.lo && pos < ld.sp.hi && ((there >> (lane / R)) & 1));
-            if (lane == 0) s_mask[warp][mask_at] = mask;
-            mask_at = (mask_at + 1) & (kMasks - 1);
+            if (lane == 0) s_mask[warp][k_next & (kMasks - 1)] = mask;
+            if (++k_next < n_steps) {
+                ld.next(a);
+                fetch_page();
+            }
+        } else {
+            ++v_next;
         }
-        if (lane == 0) mbar_arrive_expect_tx(bar, step_bytes);
+        uint64_t* bar = &s_full[warp][load_stage];
+        if (lane == 0) mbar_arrive_expect_tx(bar, is_k ? k_bytes : v_bytes);
         __syncwarp();
-        if (box_in >= 0)
-            for (int h = my_half; h < halves; h += 32 / groups)
-                tma_load_3d(dst + h * kHalfBytes + my_group * R * 128, load_unit ? &map_v : &map_k, bar, f0 + h * 64,
-                            box_in, box_row);
-        if (load_unit == 1 && ++loaded < g1) {
-            ld.next(a);
-            fetch_page();
+        const int in = is_k ? k_in : v_in, row = is_k ? k_row : v_row;
+        if (in >= 0) {
+            uint8_t* dst = ring + load_stage * unit_bytes + lane * R * 128 * halves;
+            const CUtensorMap* map = is_k ? &map_k : &map_v;
+            if (a.merged) {
+                tma_load_4d(dst, map, bar, 0, in, f0 / 64, row);
+            } else {
+                for (int h = 0; h < boxes; ++h) tma_load_3d(dst + h * R * 128, map, bar, f0 + h * 64, in, row);
+            }
         }
-        load_unit ^= 1;
         load_stage = load_stage + 1 == n_units ? 0 : load_stage + 1;
     };
     fetch_page();
     for (int i = 0; i < n_units; ++i) load_next();
 
-    const int g = lane >> 2, t2 = (lane & 3) * 2;
-    uint32_t qf[kSlice / 16][2];
-    float o[kSlice / 16][4];
-    float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;  // heads t2, t2 + 1
-    bool open = false, begins = false;
-    int stage = 0, buf = 0, mask_use = 0;
+    // ---- units in use.  Row r of a unit lies at row_at(r), its second half R rows on; 16-byte
+    // chunks are swizzled by the address's 128-byte line.
+    auto row_at = [&](int r) { return (uint32_t)((r / R) * R * halves + r % R) * 128u; };
+    const uint32_t half_at = R * 128, block_at = row_at(16);  // (16 rows on: a multiple of 1024 bytes)
+    const int k_hi = lane >> 4, v_hi = (lane >> 3) & 1;
+    const uint32_t k_at = row_at(lane & 15), v_at = row_at((lane & 7) + ((lane >> 4) << 3));
+    const uint32_t k_x[2] = {(k_at >> 7) & 7, ((k_at + half_at) >> 7) & 7};
+    const uint32_t v_x[2] = {(v_at >> 7) & 7, ((v_at + half_at) >> 7) & 7};
+    int stage = 0;
     uint32_t phase = 0;
-    // this warp's next unit has landed (false: the wait ran out)
     auto wait_unit = [&]() {
         if (!dead && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][stage], phase, kErrTimeoutLoad))) dead = true;
+        return smem_u32(ring) + stage * unit_bytes;
     };
     auto unit_done = [&]() {
         if (++stage == n_units) {
@@ -297,51 +328,143 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         __syncwarp();  // every lane has read the unit
         load_next();
     };
-    for (long long step = g0; step < g1; ++step) {
-        const int hblk = cur.hh % a.blocks, kv = cur.hh / a.blocks;
-        const int head0 = kv * a.group + hblk * 8, heads = min(8, a.group - hblk * 8);
-        if (!open) {
-            open = true;
-            begins = cur.s == cur.sp.s0;
-            const __nv_bfloat16* q = a.q + ((size_t)cur.b * a.Hq + head0 + min(g, heads - 1)) * a.D + f0;
+
+    const int g = lane >> 2, t2 = (lane & 3) * 2;
+    uint32_t qf[kSlice / 16][2];
+    float o[kSlice / 16][4];
+    float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;  // heads t2, t2 + 1
+    float sc[2][4];                                // scores: keys 16 i + g and + 8, heads t2 and t2 + 1
+    uint32_t ph[2][2], pl[2][2], mask = 0;
+    int buf = 0;
+    bool begins = cur.s == cur.sp.s0;
+    Cursor nxt = cur;
+    for (int step = -1; step < n_steps; ++step) {
+        // `cur` is at `step`, `nxt` at the step behind it
+        const bool more = step + 1 < n_steps;
+        const bool ends = step < 0 || cur.s + 1 == cur.sp.s1;  // (an item, or nothing yet)
+        if (more) {
+            if (step >= 0) nxt.next(a);
+            if (ends) {
+                const int heads = heads_of(nxt.hh);
+                const __nv_bfloat16* q = a.q + ((size_t)nxt.b * a.Hq + head0_of(nxt.hh) + min(g, heads - 1)) * a.D + f0;
 #pragma unroll
-            for (int kk = 0; kk < kSlice / 16; ++kk) {
-                const int c = kk * 16 + t2;
-                qf[kk][0] = g < heads && c < width ? *reinterpret_cast<const uint32_t*>(q + c) : 0u;
-                qf[kk][1] = g < heads && c + 8 < width ? *reinterpret_cast<const uint32_t*>(q + c + 8) : 0u;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[kk][e] = 0.f;
+                for (int kk = 0; kk < kSlice / 16; ++kk) {
+                    const int x = kk * 16 + t2;
+                    qf[kk][0] = g < heads && x < width ? *reinterpret_cast<const uint32_t*>(q + x) : 0u;
+                    qf[kk][1] = g < heads && x + 8 < width ? *reinterpret_cast<const uint32_t*>(q + x + 8) : 0u;
+                }
             }
-            m0 = m1 = -INFINITY;
-            l0 = l1 = 0.f;
-        }
-        // ---- scores of 2 x 16 keys
-        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        wait_unit();
-        {
-            const uint32_t base = smem_u32(ring) + stage * unit_bytes + (lane & 15) * 128;
-            const int r7 = lane & 7, hi = lane >> 4;
+            const uint32_t base = wait_unit() + k_at;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
 #pragma unroll
             for (int kk = 0; kk < kSlice / 16; ++kk) {
-                if (kk * 16 >= width) break;
-                const uint32_t at = base + (kk >> 2) * kHalfBytes + (((2 * (kk & 3) + hi) ^ r7) << 4);
+                if (TW == 0 && kk * 16 >= width) break;
+                const uint32_t at = base + (kk >> 2) * half_at + (((2 * (kk & 3) + k_hi) ^ k_x[kk >> 2]) << 4);
                 uint32_t ka[4], kb[4];
                 ldsm4(at, ka);
-                ldsm4(at + 16 * 128, kb);
+                ldsm4(at + block_at, kb);
                 mma_bf16(sc[0], ka, qf[kk][0], qf[kk][1]);
                 mma_bf16(sc[1], kb, qf[kk][0], qf[kk][1]);
             }
+            unit_done();
         }
-        unit_done();
-        if (a.tw > 1) {
+        if (step >= 0) {
+            const uint32_t unit = wait_unit();
+            if (mask != ~0u) {
+                // rows without a key hold what the page held (or the ring, where no box was
+                // loaded): p = 0 there must meet a finite value
+                if (!((mask >> lane) & 1)) {
+                    const uint32_t row = unit + row_at(lane);
+                    for (int c = 0; c < halves * 8; ++c)
+                        st_shared_v4(row + (c >> 3) * half_at + (c & 7) * 16, 0, 0, 0, 0);
+                    fence_proxy_async_shared();  // before the ring's next load of these bytes
+                }
+                __syncwarp();
+            }
+            const uint32_t base = unit + v_at;
+#pragma unroll
+            for (int mt = 0; mt < kSlice / 16; ++mt) {
+                if (TW == 0 && mt * 16 >= width) break;
+                const uint32_t at = base + (mt >> 2) * half_at + (((2 * (mt & 3) + v_hi) ^ v_x[mt >> 2]) << 4);
+                uint32_t va[4], vb[4];
+                ldsm4_t(at, va);
+                ldsm4_t(at + block_at, vb);
+                mma_bf16(o[mt], va, ph[0][0], ph[0][1]);
+                mma_bf16(o[mt], vb, ph[1][0], ph[1][1]);
+                mma_bf16(o[mt], va, pl[0][0], pl[0][1]);
+                mma_bf16(o[mt], vb, pl[1][0], pl[1][1]);
+            }
+            unit_done();
+            if (ends || !more) {
+                // ---- an item, or a piece of one, is done
+                float s0 = l0, s1 = l1;
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) {
+                    s0 += __shfl_xor_sync(0xffffffffu, s0, x);
+                    s1 += __shfl_xor_sync(0xffffffffu, s1, x);
+                }
+                const int heads = heads_of(cur.hh), head0 = head0_of(cur.hh);
+                const bool whole = begins && ends;
+                const float r0 = whole ? (s0 > 0.f ? 1.f / s0 : 0.f) : 1.f;
+                const float r1 = whole ? (s1 > 0.f ? 1.f / s1 : 0.f) : 1.f;
+                const int kind = begins ? 1 : 0;
+                // the last piece of the range may lie in the ring, which is idle then
+                float* part = !more ? reinterpret_cast<float*>(ring) : early;
+#pragma unroll
+                for (int mt = 0; mt < kSlice / 16; ++mt) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int head = t2 + (e & 1), x = mt * 16 + g + (e >> 1) * 8;
+                        if (head >= heads || x >= width) continue;
+                        const float val = o[mt][e] * ((e & 1) ? r1 : r0);
+                        if (!whole) {
+                            part[head * kSlice + x] = val;
+                        } else {
+                            const size_t at = ((size_t)cur.b * a.Hq + head0 + head) * a.D + f0 + x;
+                            if (a.out_f32) static_cast<float*>(a.out)[at] = val;
+                            else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(val);
+                        }
+                    }
+                }
+                if (w_in == 0 && g == 0) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int head = t2 + e;
+                        if (head >= heads) continue;
+                        const float mm = e ? m1 : m0, ll = e ? s1 : s0;
+                        if (!whole) {
+                            s_ml[team][kind][head] = mm;
+                            s_ml[team][kind][8 + head] = ll;
+                        } else if (a.lse != nullptr) {
+                            a.lse[(size_t)cur.b * a.Hq + head0 + head] =
+                                ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+                        }
+                    }
+                }
+                if (!whole && w_in == 0 && lane == 0) {
+                    s_has[team][kind] = ends ? 2 : 1;
+                    if (kind == 0) s_end[team] = !more;
+                    s_item[team][kind] = Item{cur.b, cur.hh, g0 + step - (cur.s - cur.sp.s0),
+                                              g0 + step + (cur.sp.s1 - 1 - cur.s)};
+                }
+                begins = true;  // (the next step, if any, starts an item)
+            }
+        }
+        if (!more) break;
+        cur = nxt;
+        // ---- whole scores from the team's parts
+        if (TW != 1 && tw > 1) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) exch[buf][warp][i][lane] = make_float4(sc[i][0], sc[i][1], sc[i][2], sc[i][3]);
-            team_sync(team, a.tw * 32);
+            team_sync(team, tw * 32);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float4 s = exch[buf][team * a.tw][i][lane];
-                for (int w = 1; w < a.tw; ++w) {
-                    const float4 x = exch[buf][team * a.tw + w][i][lane];
+                float4 s = exch[buf][team * tw][i][lane];
+#pragma unroll
+                for (int w = 1; w < (TW > 0 ? TW : kMaxWarps); ++w) {
+                    if (TW == 0 && w >= tw) break;
+                    const float4 x = exch[buf][team * tw + w][i][lane];
                     s.x += x.x;
                     s.y += x.y;
                     s.z += x.z;
@@ -354,17 +477,26 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             }
             buf ^= 1;
         }
-        // ---- running maximum and sum; p of keys 16 i + g and + 8, heads t2 and t2 + 1
-        const uint32_t mask = s_mask[warp][mask_use];
-        mask_use = (mask_use + 1) & (kMasks - 1);
+        // ---- running maximum and sum; p in two bf16 parts
+        if (ends) {
+            m0 = m1 = -INFINITY;
+            l0 = l1 = 0.f;
+#pragma unroll
+            for (int mt = 0; mt < kSlice / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+        }
+        mask = s_mask[warp][(step + 1) & (kMasks - 1)];
         float n0 = m0, n1 = m1;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const bool k0 = (mask >> (16 * i + g)) & 1, k1 = (mask >> (16 * i + g + 8)) & 1;
-            sc[i][0] = k0 ? sc[i][0] * a.scale_log2 : -INFINITY;
-            sc[i][1] = k0 ? sc[i][1] * a.scale_log2 : -INFINITY;
-            sc[i][2] = k1 ? sc[i][2] * a.scale_log2 : -INFINITY;
-            sc[i][3] = k1 ? sc[i][3] * a.scale_log2 : -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[i][e] *= a.scale_log2;
+            if (mask != ~0u) {
+                const bool k0 = (mask >> (16 * i + g)) & 1, k1 = (mask >> (16 * i + g + 8)) & 1;
+                sc[i][0] = k0 ? sc[i][0] : -INFINITY;
+                sc[i][1] = k0 ? sc[i][1] : -INFINITY;
+                sc[i][2] = k1 ? sc[i][2] : -INFINITY;
+                sc[i][3] = k1 ? sc[i][3] : -INFINITY;
+            }
             n0 = fmaxf(n0, fmaxf(sc[i][0], sc[i][2]));
             n1 = fmaxf(n1, fmaxf(sc[i][1], sc[i][3]));
         }
@@ -374,12 +506,20 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
         }
         const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;  // nothing seen yet
-        const float f0c = ex2f(m0 - b0), f1c = ex2f(m1 - b1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= f0c;
-        l1 *= f1c;
-        uint32_t ph[2][2], pl[2][2];
+        if (__any_sync(0xffffffffu, n0 != m0 || n1 != m1)) {  // (seldom, after the first steps)
+            const float f0c = ex2f(m0 - b0), f1c = ex2f(m1 - b1);
+            l0 *= f0c;
+            l1 *= f1c;
+#pragma unroll
+            for (int mt = 0; mt < kSlice / 16; ++mt) {
+                o[mt][0] *= f0c;
+                o[mt][1] *= f1c;
+                o[mt][2] *= f0c;
+                o[mt][3] *= f1c;
+            }
+            m0 = n0;
+            m1 = n1;
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const float p[4] = {ex2f(sc[i][0] - b0), ex2f(sc[i][1] - b1), ex2f(sc[i][2] - b0), ex2f(sc[i][3] - b1)};
@@ -393,93 +533,6 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                 ph[i][j] = movm(h);
             }
         }
-        wait_unit();
-        if (mask != ~0u) {
-            // rows without a key hold what the page held (or the ring, where no box was
-            // loaded): p = 0 there must meet a finite value
-            if (!((mask >> lane) & 1)) {
-                uint8_t* row = ring + stage * unit_bytes + lane * 128;
-                for (int c = 0; c < halves * 8; ++c)
-                    *reinterpret_cast<uint4*>(row + (c >> 3) * kHalfBytes + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                fence_proxy_async_shared();  // before the ring's next load of these bytes
-            }
-            __syncwarp();
-        }
-        {
-            const uint32_t base =
-                smem_u32(ring) + stage * unit_bytes + ((lane & 7) + ((lane >> 4) << 3)) * 128;
-            const int r7 = lane & 7, hi = (lane >> 3) & 1;
-#pragma unroll
-            for (int mt = 0; mt < kSlice / 16; ++mt) {
-                if (mt * 16 >= width) break;
-                const uint32_t at = base + (mt >> 2) * kHalfBytes + (((2 * (mt & 3) + hi) ^ r7) << 4);
-                uint32_t va[4], vb[4];
-                ldsm4_t(at, va);
-                ldsm4_t(at + 16 * 128, vb);
-                o[mt][0] *= f0c;
-                o[mt][1] *= f1c;
-                o[mt][2] *= f0c;
-                o[mt][3] *= f1c;
-                mma_bf16(o[mt], va, ph[0][0], ph[0][1]);
-                mma_bf16(o[mt], vb, ph[1][0], ph[1][1]);
-                mma_bf16(o[mt], va, pl[0][0], pl[0][1]);
-                mma_bf16(o[mt], vb, pl[1][0], pl[1][1]);
-            }
-        }
-        unit_done();
-        const bool ends = cur.s + 1 == cur.sp.s1;
-        if (ends || step + 1 == g1) {
-            // ---- a piece, or a whole item, is done
-            float t0 = l0, t1 = l1;
-#pragma unroll
-            for (int x = 4; x < 32; x <<= 1) {
-                t0 += __shfl_xor_sync(0xffffffffu, t0, x);
-                t1 += __shfl_xor_sync(0xffffffffu, t1, x);
-            }
-            const bool whole = begins && ends;
-            const float r0 = whole ? (t0 > 0.f ? 1.f / t0 : 0.f) : 1.f, r1 = whole ? (t1 > 0.f ? 1.f / t1 : 0.f) : 1.f;
-            const int dp = a.tw * kSlice;
-            float* part = a.part + (size_t)(my_team * 2 + (begins ? 1 : 0)) * piece_floats(8, dp);
-#pragma unroll
-            for (int mt = 0; mt < kSlice / 16; ++mt) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int head = t2 + (e & 1), c = mt * 16 + g + (e >> 1) * 8;
-                    if (head >= heads || c >= width) continue;
-                    const float x = o[mt][e] * ((e & 1) ? r1 : r0);
-                    if (!whole) {
-                        part[(size_t)head * dp + f0 + c] = x;
-                    } else {
-                        const size_t at = ((size_t)cur.b * a.Hq + head0 + head) * a.D + f0 + c;
-                        if (a.out_f32) static_cast<float*>(a.out)[at] = x;
-                        else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(x);
-                    }
-                }
-            }
-            if (w_in == 0 && g == 0) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int head = t2 + e;
-                    if (head >= heads) continue;
-                    const float mm = e ? m1 : m0, ll = e ? t1 : t0;
-                    if (!whole) {
-                        part[(size_t)8 * dp + head] = mm;
-                        part[(size_t)8 * dp + 8 + head] = ll;
-                    } else if (a.lse != nullptr) {
-                        a.lse[(size_t)cur.b * a.Hq + head0 + head] =
-                            ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
-                    }
-                }
-            }
-            if (step + 1 == g1 && w_in == 0 && lane == 0) {
-                // the last team of the item that this team starts and leaves unfinished
-                const long long rest = (long long)cur.sp.s1 - cur.s - 1;
-                a.jobs[my_team] = begins && !ends ? make_int4(cur.b, cur.hh, (int)((step + rest) / per), 0)
-                                                  : make_int4(-1, 0, 0, 0);
-            }
-            open = false;
-        }
-        if (step + 1 < g1) cur.next(a);
     }
     if (dead) {
         // leave no copy in flight (each wait is bounded again)
@@ -491,27 +544,71 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             }
         }
     }
-}
+    }  // n_steps > 0
 
-// Joins the pieces of the items that the teams of main CTA blockIdx.x start, for one
-// head (blockIdx.y) and 128 features (blockIdx.z; a lane has 4).  An item of up to
-// 8 pieces is joined by the warp of its team; a longer one by all warps, which
-// take pieces in turn.  The order of the sums is fixed by the sizes alone.
-constexpr int kJoinWarps = kMaxWarps;
-__global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(DecodeArgs a) {
-    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
-    __shared__ float4 s_o[kJoinWarps][32];
-    pdl_wait();
-    const int dp = a.tw * kSlice, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const size_t pf = piece_floats(8, dp);
-    const int head = blockIdx.y, c = blockIdx.z * 128 + lane * 4;
-    const bool live = c < a.D;
+    // requests without keys: their output is zero
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        const Span sp = span_of(a, b);
+        if (tid == 0 && a.lengths[b] > sp.hi) record_error(kErrBadIndex);  // longer than the table is wide
+        if (sp.steps() > 0) continue;
+        for (int i = tid; i < a.Hq * a.D; i += nthreads) {
+            const size_t at = (size_t)b * a.Hq * a.D + i;
+            if (a.out_f32) static_cast<float*>(a.out)[at] = 0.f;
+            else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(0.f);
+        }
+        if (a.lse != nullptr)
+            for (int i = tid; i < a.Hq; i += nthreads) a.lse[(size_t)b * a.Hq + i] = -INFINITY;
+    }
+    if ((long long)blockIdx.x * teams * per >= total) return;  // no steps for this CTA
 
-    auto store = [&](const int4& job, float4 acc, float top, float l) {
+    // ---- joining.  One head and 128 features of n pieces per warp, a lane four features:
+    // unnormalised sum, m and l; load_o(i) gives piece i's four features, load_ml(i, j) its m and l.
+    const int n_warps = nthreads >> 5;
+    auto join = [&](int n, auto load_o, auto load_ml, float4& acc, float& top, float& l) {
+        constexpr int kAhead = 8;
+        top = -INFINITY;
+        l = 0.f;
+        acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < n; i0 += kAhead) {
+            float4 x[kAhead];
+            float m[kAhead], li[kAhead], nt = top;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (i0 + k < n) {
+                    x[k] = load_o(i0 + k);
+                    m[k] = load_ml(i0 + k, 0);
+                    li[k] = load_ml(i0 + k, 8);
+                } else {
+                    x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    m[k] = -INFINITY;
+                    li[k] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) nt = fmaxf(nt, m[k]);
+            const float base = nt == -INFINITY ? 0.f : nt, w0 = ex2f(top - base);
+            top = nt;
+            l *= w0;
+            acc.x *= w0;
+            acc.y *= w0;
+            acc.z *= w0;
+            acc.w *= w0;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const float w = ex2f(m[k] - base);
+                l = __fmaf_rn(w, li[k], l);
+                acc.x = __fmaf_rn(w, x[k].x, acc.x);
+                acc.y = __fmaf_rn(w, x[k].y, acc.y);
+                acc.z = __fmaf_rn(w, x[k].z, acc.z);
+                acc.w = __fmaf_rn(w, x[k].w, acc.w);
+            }
+        }
+    };
+    auto store = [&](const Item& it, int head, int slice, const float4& acc, float top, float l) {
         const float r = l > 0.f ? 1.f / l : 0.f;
-        const int hblk = job.y % a.blocks, kv = job.y / a.blocks;
-        const size_t row = (size_t)job.x * a.Hq + kv * a.group + hblk * 8 + head;
-        if (live) {
+        const size_t row = (size_t)it.b * a.Hq + head0_of(it.hh) + head;
+        const int c = slice * kSlice + lane * 4;
+        if (c < a.D) {
             if (a.out_f32)
                 *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * a.D + c) =
                     make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
@@ -519,76 +616,114 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(DecodeArgs 
                 *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * a.D + c) =
                     make_uint2(pack_bf16(acc.x * r, acc.y * r), pack_bf16(acc.z * r, acc.w * r));
         }
-        if (a.lse != nullptr && blockIdx.z == 0 && lane == 0)
-            a.lse[row] = l > 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (a.lse != nullptr && c == 0) a.lse[row] = l > 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
     };
-    auto add = [](float4& acc, float w, const float4& x) {
-        acc.x = __fmaf_rn(w, x.x, acc.x);
-        acc.y = __fmaf_rn(w, x.y, acc.y);
-        acc.z = __fmaf_rn(w, x.z, acc.z);
-        acc.w = __fmaf_rn(w, x.w, acc.w);
-    };
-
-    for (int t = 0; t < a.teams; ++t) {
-        const int t0 = blockIdx.x * a.teams + t;
-        const int4 job = a.jobs[t0];
-        if (job.x < 0 || head >= min(8, a.group - job.y % a.blocks * 8)) continue;
-        const int n = job.z - t0 + 1;  // pieces: (t0, starts), (t0 + 1, goes on), ...
-        auto piece = [&](int i) { return a.part + ((size_t)(t0 + i) * 2 + (i == 0 ? 1 : 0)) * pf; };
-        if (n <= kJoinWarps) {
-            if (warp != t) continue;
-            const float m = lane < n ? piece(lane)[(size_t)8 * dp + head] : -INFINITY;
-            const float li = lane < n ? piece(lane)[(size_t)8 * dp + 8 + head] : 0.f;
-            float4 x[kJoinWarps];
-#pragma unroll
-            for (int i = 0; i < kJoinWarps; ++i)
-                if (i < n && live) x[i] = *reinterpret_cast<const float4*>(piece(i) + (size_t)head * dp + c);
-            float top = m;
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            top = __shfl_sync(0xffffffffu, top, 0);
-            const float w = ex2f(m - (top == -INFINITY ? 0.f : top));
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            float l = 0.f;
-#pragma unroll
-            for (int i = 0; i < kJoinWarps; ++i) {
-                if (i >= n) break;
-                const float wi = __shfl_sync(0xffffffffu, w, i);
-                l = __fmaf_rn(wi, __shfl_sync(0xffffffffu, li, i), l);
-                if (live) add(acc, wi, x[i]);
+    const size_t pf = piece_floats(tw);
+    __syncthreads();
+    // within the CTA: the item that comes in (t = -1), and those that a team starts and does
+    // not finish; the warps take (item, head, slice) in turn
+    Item in_item{}, out_item{};
+    bool has_in = false, has_out = false;
+    int turn = 0;
+    for (int t = -1; t < teams; ++t) {
+        const int from = t < 0 ? 0 : t, kind = t < 0 ? 0 : 1;
+        if (s_has[from][kind] == 0) continue;
+        const Item it = s_item[from][kind];
+        int n = 1;
+        bool ended = s_has[from][kind] == 2;
+        while (!ended && from + n < teams && s_has[from + n][0] != 0) {
+            ended = s_has[from + n][0] == 2;
+            ++n;
+        }
+        const bool whole = kind == 1 && ended;
+        const int tasks = heads_of(it.hh) * tw;
+        for (int q = (warp - turn % n_warps + n_warps) % n_warps; q < tasks; q += n_warps) {
+            const int head = q / tw, slice = q - head * tw;
+            // (a team's piece lies in its rings if it is the last of the team's range)
+            auto load_o = [&](int i) {
+                const int w = (from + i) * tw + slice;
+                const bool in_ring = (i == 0 && kind == 1) || s_end[from + i];
+                const float* o_p = in_ring ? reinterpret_cast<const float*>(smem + w * kRingBytes)
+                                           : early + ((long long)w - warp) *
+                                                         (a.early_floats > 0 ? a.early_floats : kSliceFloats);
+                return reinterpret_cast<const float4*>(o_p + head * kSlice)[lane];
+            };
+            auto load_ml = [&](int i, int j) { return s_ml[from + i][i == 0 ? kind : 0][j + head]; };
+            float4 acc;
+            float top, l;
+            join(n, load_o, load_ml, acc, top, l);
+            if (whole) {
+                store(it, head, slice, acc, top, l);
+            } else {
+                float* p = a.part + (size_t)(blockIdx.x * 2 + kind) * pf;
+                reinterpret_cast<float4*>(p + (size_t)slice * kSliceFloats + head * kSlice)[lane] = acc;
+                if (slice == 0 && lane == 0) {
+                    p[(size_t)tw * kSliceFloats + head] = top;
+                    p[(size_t)tw * kSliceFloats + 8 + head] = l;
+                }
             }
-            store(job, acc, top, l);
-            continue;
         }
-        float top = -INFINITY;
-        for (int i = threadIdx.x; i < n; i += kJoinWarps * 32) top = fmaxf(top, piece(i)[(size_t)8 * dp + head]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane == 0) s_m[warp] = top;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kJoinWarps; ++i) top = fmaxf(top, s_m[i]);
-        const float base = top == -INFINITY ? 0.f : top;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-#pragma unroll 8
-        for (int i = warp; i < n; i += kJoinWarps) {
-            const float* p = piece(i);
-            const float w = ex2f(p[(size_t)8 * dp + head] - base);
-            l = __fmaf_rn(w, p[(size_t)8 * dp + 8 + head], l);
-            if (live) add(acc, w, *reinterpret_cast<const float4*>(p + (size_t)head * dp + c));
-        }
-        s_o[warp][lane] = acc;
-        if (lane == 0) s_l[warp] = l;
-        __syncthreads();
-        if (warp == 0) {
-            for (int i = 1; i < kJoinWarps; ++i) {
-                add(acc, 1.f, s_o[i][lane]);
-                l += s_l[i];
+        turn += tasks;
+        if (!whole) {
+            if (kind == 0) {
+                in_item = it;
+                has_in = true;
+            } else {
+                out_item = it;
+                has_out = true;
             }
-            store(job, acc, top, l);
         }
-        __syncthreads();  // the shared sums may be written again
+    }
+    if (!has_in && !has_out) return;  // (uniform over the CTA)
+    // across CTAs: each raises the flag of its piece, then looks at the flags of all pieces of
+    // the item.  The last to raise one sees them all and joins them (so may another that
+    // looks later: it writes the same), and lowers the flags for a replay of this call.
+    const long long cta_steps = per * teams;
+    __syncthreads();
+    if (tid == 0) {
+        __threadfence();  // this CTA's pieces before their flags
+        if (has_in) *reinterpret_cast<volatile unsigned long long*>(a.flags + blockIdx.x * 2) = a.tag;
+        if (has_out) *reinterpret_cast<volatile unsigned long long*>(a.flags + blockIdx.x * 2 + 1) = a.tag;
+        __threadfence();  // and the flags before the look at the others'
+    }
+    __syncthreads();
+    // warp 0 looks at the item that goes out, warp 1 (or 0) at the one that comes in
+    for (int kind = 1; kind >= 0; --kind) {
+        if (warp != (kind == 1 || n_warps == 1 ? 0 : 1)) continue;
+        bool all = kind ? has_out : has_in;
+        const Item it = kind ? out_item : in_item;
+        const int c0 = (int)(it.first / cta_steps), n = all ? (int)(it.last / cta_steps) - c0 + 1 : 0;
+        for (int i = lane; i < n; i += 32)
+            all = all && *reinterpret_cast<volatile unsigned long long*>(
+                             a.flags + (size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) == a.tag;
+        all = __all_sync(0xffffffffu, all);
+        if (lane == 0) s_last[kind] = all;
+        __threadfence();  // the others' pieces after their flags
+    }
+    __syncthreads();
+    turn = 0;
+    for (int kind = 1; kind >= 0; --kind) {
+        if (!s_last[kind]) continue;
+        const Item it = kind ? out_item : in_item;
+        const int c0 = (int)(it.first / cta_steps), n = (int)(it.last / cta_steps) - c0 + 1;
+        auto index = [&](int i) { return (size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0); };
+        const int tasks = heads_of(it.hh) * tw;
+        for (int q = (warp - turn % n_warps + n_warps) % n_warps; q < tasks; q += n_warps) {
+            const int head = q / tw, slice = q - head * tw;
+            float4 acc;
+            float top, l;
+            // (written by other SMs while this kernel runs: past L1)
+            join(n,
+                 [&](int i) {
+                     return __ldcg(reinterpret_cast<const float4*>(a.part + index(i) * pf +
+                                                                   (size_t)slice * kSliceFloats + head * kSlice) + lane);
+                 },
+                 [&](int i, int j) { return __ldcg(a.part + index(i) * pf + (size_t)tw * kSliceFloats + j + head); },
+                 acc, top, l);
+            store(it, head, slice, acc, top, l);
+        }
+        turn += tasks;
+        for (int i = tid; i < n; i += nthreads) a.flags[index(i)] = 0;
     }
 }
 
