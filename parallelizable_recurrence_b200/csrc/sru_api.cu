@@ -291,6 +291,26 @@ sru_status check_layer_sizes(int64_t L, int64_t B, int64_t d) {
 
 inline unsigned blocks_for(size_t n, unsigned threads) { return (unsigned)((n + threads - 1) / threads); }
 
+// ---------------------------------------------------------- overlapped launch
+// Launch of a kernel that calls pdl_wait before it touches memory: it may start while the
+// kernel before it on the stream runs out.
+template <typename... Params, typename... Args>
+sru_status launch_overlapped(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
+                                    const Args&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    SRU_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, args...));
+    return SRU_OK;
+}
+
 // ------------------------------------------------------------- GEMM launch
 // The CTA-pair kernel: 256 x 256 output tiles over two SMs; a K-major B
 // operand is staged as 128 rows per CTA.
@@ -299,12 +319,14 @@ constexpr uint32_t kGemmBRows = (uint32_t)sru::gemm::P_CN;
 // tail_split (pair kernel, OUT == kOutF32 only): the output tiles of the last,
 // partial round of CTA pairs are cut in two k-pieces that add onto regions
 // zeroed here first (see sru::gemm::pair_next).
-template <bool A_MN, bool B_MN, int OUT>
+// CHAIN: an overlapped launch whose output is multiplied by *scale (device memory).
+template <bool A_MN, bool B_MN, int OUT, bool CHAIN = false>
 sru_status launch_tc_gemm(const CUtensorMap& ma, const CUtensorMap& mb, void* out, int64_t R, int64_t C,
-                          int64_t Kr, cudaStream_t st, int splits = 1, int64_t ldo = -1, bool tail_split = false) {
+                          int64_t Kr, cudaStream_t st, int splits = 1, int64_t ldo = -1, bool tail_split = false,
+                          const float* scale = nullptr) {
     if (ldo < 0) ldo = C;
     {
-        auto kern = sru::gemm::tc_gemm_pair_kernel<A_MN, B_MN, OUT>;
+        auto kern = sru::gemm::tc_gemm_pair_kernel<A_MN, B_MN, OUT, 0, 0, 0, 0, CHAIN>;
         SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kern), sru::gemm::P_SMEM_BYTES));
         // the output as the epilogue's TMA store target: boxes of 32 rows x 128 bytes
         // (64 bf16 or 32 fp32 columns), swizzled like the staging buffers
@@ -340,8 +362,11 @@ sru_status launch_tc_gemm(const CUtensorMap& ma, const CUtensorMap& mb, void* ou
                                                                    (long long)ldo, (int)n_tiles, (int)(F * pairs));
             SRU_CUDA_TRY(cudaGetLastError());
         }
+        if (CHAIN)
+            return launch_overlapped(kern, dim3((unsigned)(2 * pairs)), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st,
+                                     ma, mb, mo, (int)R, (int)C, (int)Kr, splits, 1, tail_s, 0, scale);
         kern<<<(unsigned)(2 * pairs), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st>>>(
-            ma, mb, mo, (int)R, (int)C, (int)Kr, splits, 1, tail_s, 0);
+            ma, mb, mo, (int)R, (int)C, (int)Kr, splits, 1, tail_s, 0, nullptr);
     }
     SRU_CUDA_TRY(cudaGetLastError());
     return SRU_OK;
@@ -386,7 +411,7 @@ sru_status launch_batched_bpo(const CUtensorMap& ma, const CUtensorMap& mb, void
             return SRU_ERR_INVALID;
     }
     kern<<<(unsigned)(2 * pairs), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st>>>(
-        ma, mb, mo, (int)R, (int)C, (int)Kr, 1, (int)batches, 0, 0);
+        ma, mb, mo, (int)R, (int)C, (int)Kr, 1, (int)batches, 0, 0, nullptr);
     SRU_CUDA_TRY(cudaGetLastError());
     return SRU_OK;
 }
@@ -1323,7 +1348,7 @@ static sru_status project_dW_split(const void* dU, const void* X, float* dW, int
     const int64_t units = tiles * pl.splits;
     const int64_t pairs = units < sm_count() / 2 ? units : sm_count() / 2;
     kern<<<(unsigned)(2 * pairs), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st>>>(
-        ma, mb, mo, (int)N, (int)K, (int)M, (int)pl.splits, 1, 0, (int)pl.slab_rows);
+        ma, mb, mo, (int)N, (int)K, (int)M, (int)pl.splits, 1, 0, (int)pl.slab_rows, nullptr);
     SRU_CUDA_TRY(cudaGetLastError());
     const size_t n4 = (size_t)N * K / 4;
     sru::gemm::splitk_reduce_kernel<<<(unsigned)std::min<size_t>(blocks_for(n4, 256), (size_t)sm_count() * 8), 256, 0,
@@ -1731,15 +1756,21 @@ sru_status sru_decode_step(const void* X_t, const void* W, const float* x_t, con
 // gradients read each piece twice; a smaller piece costs one more read and write
 // of the M x K fp32 sum dH, a larger one memory.
 constexpr size_t kLossPieceBytes = (size_t)512 << 20;
+// Reduction below which the vocabulary product has eight epilogue warps.  Measured, M4096
+// V32000, loss: 4 / 8 warps 97 / 84 us at K128, 98 / 91 at K256, 112 / 111-114 at K512, 148-151 /
+// 158-164 at K768.
+constexpr int64_t kLossShortK = 384;
 struct LossPlan {
-    int64_t n_tiles, Vc, pieces;
+    int warps;                   // epilogue warps of the vocabulary product
+    int64_t parts, Vc, pieces;   // parts of the statistics; piece width and number
     SplitPlan dh, dw;
-    size_t partial_off, target_off, dz_off, dh_off, dw_off, forward_total, total;
+    size_t partial_off, target_off, scale_off, dz_off, dh_off, dw_off, forward_total, total;
 };
 static LossPlan loss_plan(int64_t M, int64_t V, int64_t K, bool backward) {
     LossPlan p{};
-    p.n_tiles = (V + sru::gemm::P_BN - 1) / sru::gemm::P_BN;
-    p.target_off = round256((size_t)p.n_tiles * M * sizeof(float2));
+    p.warps = K < kLossShortK ? 8 : 4;
+    p.parts = p.warps / 4 * ((V + sru::gemm::P_BN - 1) / sru::gemm::P_BN);
+    p.target_off = round256((size_t)p.parts * M * sizeof(float2));
     p.forward_total = p.target_off + round256((size_t)M * 4);
     p.total = p.forward_total;
     if (!backward) return p;
@@ -1750,7 +1781,8 @@ static LossPlan loss_plan(int64_t M, int64_t V, int64_t K, bool backward) {
     p.pieces = (V + p.Vc - 1) / p.Vc;
     p.dh = split_plan(M, K, std::min(p.Vc, V));
     p.dw = split_plan(std::min(p.Vc, V), K, M);
-    p.dh_off = round256((size_t)M * p.Vc * 2);
+    p.dz_off = 256;  // behind the weights' scale
+    p.dh_off = p.dz_off + round256((size_t)M * p.Vc * 2);
     p.dw_off = p.dh_off + round256(p.dh.splits > 1 ? p.dh.bytes : (p.pieces > 1 ? (size_t)M * K * 4 : 0));
     p.total = std::max(p.forward_total, p.dw_off + round256(p.dw.bytes));
     return p;
@@ -1765,22 +1797,27 @@ static sru_status check_loss_sizes(int64_t M, int64_t V, int64_t K) {
         return SRU_ERR_UNSUPPORTED;
     return SRU_OK;
 }
-template <int EPI>
-static sru_status launch_vocab(const CUtensorMap& mh, const CUtensorMap& mw, const CUtensorMap& mdz,
-                               const sru::loss::LossArgs& a, int64_t M, int64_t N, int64_t K, cudaStream_t st) {
-    auto kern = sru::loss::vocab_gemm_kernel<EPI>;
+template <int EPI, int W>
+static sru_status launch_vocab_w(const CUtensorMap& mh, const CUtensorMap& mw, const CUtensorMap& mdz,
+                                 const sru::loss::LossArgs& a, int64_t M, int64_t N, int64_t K, cudaStream_t st) {
+    auto kern = sru::loss::vocab_gemm_kernel<EPI, W>;
     SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kern), sru::gemm::P_SMEM_BYTES));
     const int64_t units = ((M + sru::gemm::P_BM - 1) / sru::gemm::P_BM) * ((N + sru::gemm::P_BN - 1) / sru::gemm::P_BN);
     const int64_t pairs = std::min<int64_t>(units, sm_count() / 2);
-    kern<<<(unsigned)(2 * pairs), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st>>>(mh, mw, mdz, a, (int)M, (int)N,
-                                                                                     (int)K);
-    SRU_CUDA_TRY(cudaGetLastError());
-    return SRU_OK;
+    return launch_overlapped(kern, dim3((unsigned)(2 * pairs)), 64 + W * 32, sru::gemm::P_SMEM_BYTES, st, mh, mw, mdz, a,
+                             (int)M, (int)N, (int)K);
+}
+template <int EPI>
+static sru_status launch_vocab(int warps, const CUtensorMap& mh, const CUtensorMap& mw, const CUtensorMap& mdz,
+                               const sru::loss::LossArgs& a, int64_t M, int64_t N, int64_t K, cudaStream_t st) {
+    return warps == 8 ? launch_vocab_w<EPI, 8>(mh, mw, mdz, a, M, N, K, st)
+                      : launch_vocab_w<EPI, 4>(mh, mw, mdz, a, M, N, K, st);
 }
 template <bool A_MN, bool B_MN, int OUT>
 static sru_status launch_slabs(const CUtensorMap& ma, const CUtensorMap& mb, void* slabs, int64_t R, int64_t C,
-                               int64_t Kr, int64_t splits, int64_t slab_rows, int64_t all_splits, cudaStream_t st) {
-    auto kern = sru::gemm::tc_gemm_pair_kernel<A_MN, B_MN, OUT>;
+                               int64_t Kr, int64_t splits, int64_t slab_rows, int64_t all_splits, const float* scale,
+                               cudaStream_t st) {
+    auto kern = sru::gemm::tc_gemm_pair_kernel<A_MN, B_MN, OUT, 0, 0, 0, 0, true>;
     SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kern), sru::gemm::P_SMEM_BYTES));
     CUtensorMap mo;
     const uint64_t dims[2] = {(uint64_t)C, (uint64_t)(slab_rows * all_splits)};
@@ -1791,10 +1828,8 @@ static sru_status launch_slabs(const CUtensorMap& ma, const CUtensorMap& mb, voi
     const int64_t units =
         ((R + sru::gemm::P_BM - 1) / sru::gemm::P_BM) * ((C + sru::gemm::P_BN - 1) / sru::gemm::P_BN) * splits;
     const int64_t pairs = std::min<int64_t>(units, sm_count() / 2);
-    kern<<<(unsigned)(2 * pairs), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st>>>(
-        ma, mb, mo, (int)R, (int)C, (int)Kr, (int)splits, 1, 0, (int)slab_rows);
-    SRU_CUDA_TRY(cudaGetLastError());
-    return SRU_OK;
+    return launch_overlapped(kern, dim3((unsigned)(2 * pairs)), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st, ma, mb,
+                             mo, (int)R, (int)C, (int)Kr, (int)splits, 1, 0, (int)slab_rows, scale);
 }
 static sru_status sum_slabs(const void* slabs, void* out, int out_t, int64_t R, int64_t C, int64_t slab_rows,
                             int64_t splits, cudaStream_t st) {
@@ -1802,13 +1837,11 @@ static sru_status sum_slabs(const void* slabs, void* out, int out_t, int64_t R, 
     const unsigned grid = (unsigned)std::min<size_t>(blocks_for(n4, 256), (size_t)sm_count() * 8);
     const float4* s = static_cast<const float4*>(slabs);
     if (out_t == SRU_BF16)
-        sru::loss::slab_sum_kernel<<<grid, 256, 0, st>>>(s, static_cast<__nv_bfloat16*>(out), (int)R, (int)(C / 4),
-                                                         (long long)slab_rows, (int)splits);
-    else
-        sru::loss::slab_sum_kernel<<<grid, 256, 0, st>>>(s, static_cast<float*>(out), (int)R, (int)(C / 4),
-                                                         (long long)slab_rows, (int)splits);
-    SRU_CUDA_TRY(cudaGetLastError());
-    return SRU_OK;
+        return launch_overlapped(sru::loss::slab_sum_kernel<__nv_bfloat16>, dim3(grid), 256, 0, st, s,
+                                 static_cast<__nv_bfloat16*>(out), (int)R, (int)(C / 4), (long long)slab_rows,
+                                 (int)splits);
+    return launch_overlapped(sru::loss::slab_sum_kernel<float>, dim3(grid), 256, 0, st, s, static_cast<float*>(out),
+                             (int)R, (int)(C / 4), (long long)slab_rows, (int)splits);
 }
 static sru_status zero_typed(void* p, int t, size_t n, cudaStream_t st) {
     SRU_CUDA_TRY(cudaMemsetAsync(p, 0, n * (t == SRU_BF16 ? 2 : 4), st));
@@ -1841,13 +1874,11 @@ sru_status sru_softmax_loss(const void* H, const void* W, const int64_t* targets
     a.partial = reinterpret_cast<float2*>(ws + p.partial_off);
     a.target_logit = reinterpret_cast<float*>(ws + p.target_off);
     a.V = V;
-    s = launch_vocab<sru::loss::kStats>(mh, mw, mh, a, M, V, K, st);
+    s = launch_vocab<sru::loss::kStats>(p.warps, mh, mw, mh, a, M, V, K, st);
     if (s != SRU_OK) return s;
-    sru::loss::vocab_loss_kernel<<<blocks_for((size_t)M, sru::loss::kJoinRows),
-                                   sru::loss::kJoinRows * sru::loss::kJoinGroups, 0, st>>>(
-        a.partial, a.target_logit, a.targets, loss, lse, (int)M, (int)p.n_tiles, (long long)V);
-    SRU_CUDA_TRY(cudaGetLastError());
-    return SRU_OK;
+    return launch_overlapped(sru::loss::vocab_loss_kernel, dim3(blocks_for((size_t)M, sru::loss::kJoinRows)),
+                             sru::loss::kJoinRows * sru::loss::kJoinGroups, 0, st, a.partial, a.target_logit, a.targets,
+                             loss, lse, (int)M, (int)p.parts, (long long)V);
 }
 
 sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t* targets, const float* lse,
@@ -1878,6 +1909,11 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
     a.lse = lse;
     a.dloss = dloss;
     a.V = V;
+    float* scale = reinterpret_cast<float*>(ws + p.scale_off);
+    a.scale = scale;
+    s = launch_overlapped(sru::loss::loss_scale_kernel, dim3(1), 1024, 0, st, dloss, a.targets, scale, (int)M,
+                          (long long)V);
+    if (s != SRU_OK) return s;
     // dH is summed over the pieces in fp32: in place, or in the workspace when it is split
     // along the vocabulary or leaves as bf16
     const bool h_in_slabs = p.dh.splits > 1 || (p.pieces > 1 && dh_t == SRU_BF16);
@@ -1897,7 +1933,7 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
                 return SRU_ERR_INVALID;
         }
         a.v0 = v0;
-        s = launch_vocab<sru::loss::kGrad>(mh, mw, mdz, a, M, n, K, st);
+        s = launch_vocab<sru::loss::kGrad>(p.warps, mh, mw, mdz, a, M, n, K, st);
         if (s != SRU_OK) return s;
         if (dH) {
             // dH += dz W: A = dz (M x n) K-major, B(c = k, red = v) = W[v][k] MN-major
@@ -1908,15 +1944,15 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
                 const int64_t kb = (n + sru::gemm::BK - 1) / sru::gemm::BK;
                 const int64_t per = (kb + p.dh.splits - 1) / p.dh.splits, S = (kb + per - 1) / per;
                 s = v0 == 0 ? launch_slabs<false, true, kOutF32>(ma, mb, slab_h, M, K, n, S, p.dh.slab_rows,
-                                                                 p.dh.splits, st)
+                                                                 p.dh.splits, scale, st)
                             : launch_slabs<false, true, kOutF32Acc>(ma, mb, slab_h, M, K, n, S, p.dh.slab_rows,
-                                                                    p.dh.splits, st);
+                                                                    p.dh.splits, scale, st);
             } else {
                 void* out = h_in_slabs ? slab_h : dH;
-                if (v0 != 0) s = launch_tc_gemm<false, true, kOutF32Acc>(ma, mb, out, M, K, n, st);
+                if (v0 != 0) s = launch_tc_gemm<false, true, kOutF32Acc, true>(ma, mb, out, M, K, n, st, 1, -1, false, scale);
                 else if (!h_in_slabs && dh_t == SRU_BF16)
-                    s = launch_tc_gemm<false, true, kOutBF16>(ma, mb, out, M, K, n, st);
-                else s = launch_tc_gemm<false, true, kOutF32>(ma, mb, out, M, K, n, st, 1, -1, /*tail_split=*/true);
+                    s = launch_tc_gemm<false, true, kOutBF16, true>(ma, mb, out, M, K, n, st, 1, -1, false, scale);
+                else s = launch_tc_gemm<false, true, kOutF32, true>(ma, mb, out, M, K, n, st, 1, -1, /*tail_split=*/true, scale);
             }
             if (s != SRU_OK) return s;
         }
@@ -1926,12 +1962,12 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
             void* out = static_cast<uint8_t*>(dW) + (size_t)v0 * K * (dw_t == SRU_BF16 ? 2 : 4);
             if (p.dw.splits > 1) {
                 s = launch_slabs<true, true, kOutF32>(ma, mb, slab_w, n, K, M, p.dw.splits, p.dw.slab_rows,
-                                                      p.dw.splits, st);
+                                                      p.dw.splits, scale, st);
                 if (s == SRU_OK) s = sum_slabs(slab_w, out, dw_t, n, K, p.dw.slab_rows, p.dw.splits, st);
             } else if (dw_t == SRU_BF16) {
-                s = launch_tc_gemm<true, true, kOutBF16>(ma, mb, out, n, K, M, st);
+                s = launch_tc_gemm<true, true, kOutBF16, true>(ma, mb, out, n, K, M, st, 1, -1, false, scale);
             } else {
-                s = launch_tc_gemm<true, true, kOutF32>(ma, mb, out, n, K, M, st, 1, -1, /*tail_split=*/true);
+                s = launch_tc_gemm<true, true, kOutF32, true>(ma, mb, out, n, K, M, st, 1, -1, /*tail_split=*/true, scale);
             }
             if (s != SRU_OK) return s;
         }
@@ -1940,30 +1976,7 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
     return SRU_OK;
 }
 
-}  // extern "C"
-
 // ---- paged key/value cache and the attention of one new token over it
-// Launch of a kernel that calls pdl_wait before it touches memory: it may start while the
-// kernel before it on the stream runs out.
-template <typename... Params, typename... Args>
-static sru_status launch_overlapped(void (*kern)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st,
-                                    const Args&... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    SRU_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, args...));
-    return SRU_OK;
-}
-
-extern "C" {
-
 static sru_status check_cache_sizes(int64_t pages, int64_t ps) {
     if (pages < 0 || ps < 1) return SRU_ERR_INVALID;
     if (pages >= ((int64_t)1 << 31) || ps >= ((int64_t)1 << 31) || pages * ps >= ((int64_t)1 << 31))

@@ -10,10 +10,13 @@
 // logits of one row, so each epilogue thread reduces its row alone, without
 // shuffles.  Two epilogues:
 //   kStats  running maximum and sum of exponentials of the row's 256 logits
-//           (8 bytes per row and tile; vocab_loss_kernel joins the tiles) and,
-//           in the one tile that holds it, the target's logit;
+//           (8 bytes per row and part; vocab_loss_kernel joins them) and, in
+//           the one that holds it, the target's logit;
 //   kGrad   dz of the tile from the row's lse and weight g, rounded to bf16 as
 //           the operand of the two gradient products, stored by TMA.
+// Four epilogue warps (a thread per row), or eight (two per row) for a short
+// reduction, whose product takes less time than one warp per scheduler needs for a
+// tile's exponentials.
 // The gradients run over pieces of the vocabulary, so that dz never takes more
 // than a bounded buffer; z is recomputed there (2 M V K operations on top of
 // the gradients' 4 M V K), since reading it back in fp32 and writing it costs
@@ -36,6 +39,16 @@ __device__ __forceinline__ float ex2_approx(float x) {
     return y;
 }
 
+// r[i] without an indexed (hence local-memory) array.
+template <int NC>
+__device__ __forceinline__ float pick(const uint32_t (&r)[NC], int i) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int e = 0; e < NC; ++e)
+        asm("{\n\t.reg .pred p;\n\tsetp.eq.s32 p, %1, %2;\n\t@p mov.b32 %0, %3;\n\t}" : "+r"(v) : "r"(i), "r"(e), "r"(r[e]));
+    return __uint_as_float(v);
+}
+
 // Tiles in groups of kGroupM row tiles, the row tile fastest: the 74 pairs of a
 // round then cover about 8 x 9 tiles, and a piece of W is read from memory once
 // per group of 2048 rows instead of once per 256.
@@ -49,16 +62,18 @@ __device__ __forceinline__ void unit_tile(int u, int m_tiles, int n_tiles, int& 
 
 struct LossArgs {
     const long long* targets;  // (M): the class of each row; negative = not counted
-    float2* partial;           // kStats: (n_tiles, M) maximum and sum of exponentials
+    float2* partial;           // kStats: (parts of tiles, M) maximum and sum of exponentials
     float* target_logit;       // kStats: (M)
     const float* lse;          // kGrad: (M)
     const float* dloss;        // kGrad: (M)
+    const float* scale;        // kGrad: dz is taken over it (see loss_scale_kernel)
     long long v0, V;           // first column of this piece of the vocabulary, its whole size
 };
 
 // M rows, N columns of this piece, K the reduction.  map_w starts at row v0 of W.
-template <int EPI>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+// W = 4 or 8 epilogue warps.
+template <int EPI, int W>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + W * 32, 1)
     vocab_gemm_kernel(const __grid_constant__ CUtensorMap map_h, const __grid_constant__ CUtensorMap map_w,
                       const __grid_constant__ CUtensorMap map_dz, LossArgs a, int M, int N, int K) {
     extern __shared__ uint8_t smem_raw[];
@@ -87,7 +102,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], 8);  // 4 epilogue warps of each CTA
+            mbar_init(&tempty[i], 2 * W);  // the epilogue warps of both CTAs
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -107,6 +122,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t tmem_base = *tmem_slot;
     const uint32_t leader_full0 = mapa_shared(smem_u32(&full[0]), 0);
     const uint32_t leader_tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    pdl_launch();
+    pdl_wait();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -184,9 +201,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         }
     } else {
         // ---------------------------------------------------------- epilogue (both CTAs)
-        const int quarter = warp & 3;
+        constexpr int kParts = W / 4, kCols = P_BN / kParts;  // column parts of a tile, and their width
+        constexpr int kBufs = 8 / W;                          // staging buffers per warp
+        const int quarter = warp & 3, part = (warp - 2) >> 2;
+        uint8_t* bufs = epi + (size_t)(warp - 2) * kBufs * P_EPI_BUF;
         int it = 0;
         uint32_t nstaged = 0;
+        const float scale = EPI == kGrad ? *a.scale : 1.f;
         for (int u = pair_id; u < units; u += n_pairs, ++it) {
             int tm, tn;
             unit_tile(u, m_tiles, n_tiles, tm, tn);
@@ -197,11 +218,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             // the row's operands, fetched while the product runs
             long long tgt = live ? a.targets[row] : -1;
             if (tgt >= a.V) tgt = -1;  // not a class: vocab_loss_kernel reports it
-            const long long trel = tgt < 0 ? -1 : tgt - a.v0 - n0;  // target's column in this tile, if inside
+            // target's column in this warp's part of the tile, if inside
+            const long long trel = tgt < 0 ? -1 : tgt - a.v0 - n0 - part * kCols;
             float lse2 = 0.f, g = 0.f;
             if (EPI == kGrad && tgt >= 0) {
                 lse2 = a.lse[row] * kLog2e;
-                g = a.dloss[row];
+                g = __fdiv_rn(a.dloss[row], scale);
             }
             const bool ok = mbar_wait(&tfull[acc], (it >> 1) & 1, kErrTimeoutMma);
             if (!__all_sync(0xffffffffu, ok) || *abort_flag) {
@@ -209,20 +231,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 break;
             }
             tc_fence_after_sync();
-            constexpr int NC = 64, NG = P_BN / NC;
-            const int ncol = min(P_BN, N - n0);
-            const int ng = (ncol + NC - 1) / NC;
-            const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * P_BN;
+            constexpr int NC = EPI == kStats && W == 8 ? 32 : 64, NG = kCols / NC;
+            const int col0 = n0 + part * kCols;
+            const int ncol = max(0, min(kCols, N - col0));
+            const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * P_BN + part * kCols;
             float top = -INFINITY, sum = 0.f;
             uint32_t r0[NC], r1[NC];
             tmem_ld_cols<NC>(tacc, r0);
 #pragma unroll
             for (int c = 0; c < NG; ++c) {
-                if (c >= ng) break;  // uniform across the warp
                 uint32_t(&cur)[NC] = (c & 1) ? r1 : r0;
                 uint32_t(&nxt)[NC] = (c & 1) ? r0 : r1;
                 tc_wait_ld();
-                if (c + 1 < ng) tmem_ld_cols<NC>(tacc + (c + 1) * NC, nxt);
+                if (c + 1 < NG) tmem_ld_cols<NC>(tacc + (c + 1) * NC, nxt);
                 const long long tc = trel - c * NC;
                 const bool has_target = tc >= 0 && tc < NC;
                 if (EPI == kStats) {
@@ -243,51 +264,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         s[e & 3] += ex2_approx(__fmaf_rn(__uint_as_float(cur[e]), kLog2e, -base));
                     sum = __fmaf_rn(sum, ex2_approx(__fmaf_rn(top, kLog2e, -base)), (s[0] + s[1]) + (s[2] + s[3]));
                     top = nt;
-                    if (has_target) {
-                        float zt = 0.f;
-#pragma unroll
-                        for (int e = 0; e < NC; ++e)
-                            if (e == (int)tc) zt = __uint_as_float(cur[e]);
-                        a.target_logit[row] = zt;
-                    }
+                    if (has_target) a.target_logit[row] = pick(cur, (int)tc);
                 } else {
 #pragma unroll
                     for (int e = 0; e < NC; ++e) {
                         const float p = ex2_approx(__fmaf_rn(__uint_as_float(cur[e]), kLog2e, -lse2)) * g;
                         cur[e] = g == 0.f ? 0u : __float_as_uint(p);  // rows not counted: exactly 0
                     }
-                    float pt = 0.f;
-                    if (has_target) {
-#pragma unroll
-                        for (int e = 0; e < NC; ++e)
-                            if (e == (int)tc) pt = __uint_as_float(cur[e]);
-                    }
-                    const uint32_t buf = smem_u32(epi) + (uint32_t)(quarter * 2 + (nstaged & 1)) * P_EPI_BUF;
-                    if (nstaged >= 2) {
-                        if (lane == 0) bulk_wait_group_read<1>();
-                        __syncwarp();
-                    }
-                    epilogue_stage_row<kOutBF16>(buf, lane, cur);
+                    const float pt = has_target ? pick(cur, (int)tc) : 0.f;
+                    if (c * NC >= ncol) continue;  // (uniform across the warp)
+                    uint8_t* stage_buf = bufs + (nstaged++ % kBufs) * P_EPI_BUF;
+                    if (lane == 0) bulk_wait_group_read<kBufs - 1>();  // its last store has read it
+                    __syncwarp();
+                    epilogue_stage_row<kOutBF16>(smem_u32(stage_buf), lane, cur);
                     if (has_target) {
                         // (element tc of row `lane` in the staging buffer's swizzle)
                         const uint32_t off = lane * 128u + ((((uint32_t)tc >> 3) ^ (lane & 7u)) << 4) + (tc & 7) * 2u;
-                        *reinterpret_cast<__nv_bfloat16*>(epi + (size_t)(quarter * 2 + (nstaged & 1)) * P_EPI_BUF +
-                                                          off) = __float2bfloat16_rn(pt - g);
+                        *reinterpret_cast<__nv_bfloat16*>(stage_buf + off) = __float2bfloat16_rn(pt - g);
                     }
                     fence_proxy_async_shared();
                     __syncwarp();
                     if (lane == 0) {
-                        tma_store_2d(&map_dz, epi + (size_t)(quarter * 2 + (nstaged & 1)) * P_EPI_BUF, n0 + c * NC,
-                                     m0 + quarter * 32);
+                        tma_store_2d(&map_dz, stage_buf, col0 + c * NC, m0 + quarter * 32);
                         bulk_commit_group();
                     }
-                    ++nstaged;
                 }
             }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(leader_tempty0 + (uint32_t)acc * 8u);
-            if (EPI == kStats && live) a.partial[(size_t)tn * M + row] = make_float2(top, sum);
+            if (EPI == kStats && live) a.partial[(size_t)(kParts * tn + part) * M + row] = make_float2(top, sum);
         }
         if (EPI == kGrad && lane == 0) bulk_wait_group<0>();
     }
@@ -300,6 +306,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
 }
 
+// The largest weight of a counted row (1 if there is none, or no finite one).  dz is
+// held over it, and the gradients are multiplied by it in fp32: with the usual equal
+// weights 1 / n, every dz of a target is then p - 1 rounded to bf16, whose error
+// differs from row to row, and not -1 / n, whose error would be the same in all
+// rows and scale the whole gradient by up to 2^-9.
+__global__ void __launch_bounds__(1024) loss_scale_kernel(const float* __restrict__ dloss,
+                                                          const long long* __restrict__ targets,
+                                                          float* __restrict__ scale, int M, long long V) {
+    __shared__ float part[32];
+    pdl_launch();
+    pdl_wait();
+    float top = 0.f;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < M; i += 1024) {
+        const long long t = targets[i];
+        const float g = fabsf(dloss[i]);
+        if (t >= 0 && t < V && g < INFINITY) top = fmaxf(top, g);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    top = part[threadIdx.x];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (threadIdx.x == 0) *scale = top > 0.f ? top : 1.f;
+}
+
 // Joins a row's tiles: lse = m + log sum_t s_t exp(m_t - m) with m the largest
 // m_t; loss = lse - z_target, 0 for rows that are not counted.  32 rows x 32
 // tile groups per CTA (consecutive threads read consecutive rows).
@@ -307,8 +342,10 @@ constexpr int kJoinRows = 32, kJoinGroups = 32;
 __global__ void __launch_bounds__(kJoinRows* kJoinGroups)
     vocab_loss_kernel(const float2* __restrict__ partial, const float* __restrict__ target_logit,
                       const long long* __restrict__ targets, float* __restrict__ loss, float* __restrict__ lse,
-                      int M, int n_tiles, long long V) {
+                      int M, int parts, long long V) {
     __shared__ float2 part[kJoinGroups][kJoinRows + 1];
+    pdl_launch();
+    pdl_wait();
     const int r = threadIdx.x % kJoinRows, q = threadIdx.x / kJoinRows;
     const int row = blockIdx.x * kJoinRows + r;
     float top = -INFINITY, sum = 0.f;
@@ -320,7 +357,7 @@ __global__ void __launch_bounds__(kJoinRows* kJoinGroups)
     };
     if (row < M) {
 #pragma unroll 4
-        for (int t = q; t < n_tiles; t += kJoinGroups) join(partial[(size_t)t * M + row]);
+        for (int t = q; t < parts; t += kJoinGroups) join(partial[(size_t)t * M + row]);
     }
     part[q][r] = make_float2(top, sum);
     __syncthreads();
@@ -338,6 +375,8 @@ __global__ void __launch_bounds__(kJoinRows* kJoinGroups)
 template <typename OutT>
 __global__ void __launch_bounds__(256) slab_sum_kernel(const float4* __restrict__ slabs, OutT* __restrict__ out,
                                                        int R, int C4, long long slab_rows, int splits) {
+    pdl_launch();
+    pdl_wait();
     const size_t n = (size_t)R * C4;
     for (size_t e = blockIdx.x * (size_t)256 + threadIdx.x; e < n; e += (size_t)gridDim.x * 256) {
         float4 acc = slabs[e];
