@@ -458,7 +458,8 @@ sru_status sru_cache_append(const void* K, int64_t k_ld, const void* V, int64_t 
  * Scores, sums and the result are fp32; p enters the product with v in 16 bits
  * of precision.  A page index outside [0, pages) leaves its keys out, a length
  * beyond max_pages * page_size is cut there; both are reported as SRU_ERR_INVALID
- * by the next sru_sync_status().
+ * by the next sru_sync_status(), and so is a call whose requests need 2^30 steps or
+ * more (32 keys of one head; it writes nothing).
  * workspace: >= sru_attention_decode_workspace_bytes(B, Hq, Hkv, D) bytes; calls
  * that may run at the same time need one each.  The sums' order depends on the
  * lengths and sizes alone: the same bits every run.

@@ -2050,14 +2050,19 @@ sru_status sru_cache_append(const void* K, int64_t k_ld, const void* V, int64_t 
 
 constexpr int64_t kDecodeMaxD = (int64_t)sru::cache::kSlice * sru::cache::kMaxWarps;
 struct DecodePlan {
-    int tw, teams, blocks;
+    int width, tw, teams, blocks, units;  // features per warp, warps per team, teams per CTA, ...
     size_t flags_off, total;
 };
 static DecodePlan decode_plan(int64_t Hq, int64_t Hkv, int64_t D) {
     DecodePlan p{};
-    p.tw = (int)((D + sru::cache::kSlice - 1) / sru::cache::kSlice);
+    // 64 features per warp for D = 64, else 128 (D192, B64 H2 len <= 4000: 58 us as 128 + 64, 71 us
+    // as 3 x 64)
+    p.width = D == 64 ? 64 : sru::cache::kSlice;
+    p.tw = (int)((D + p.width - 1) / p.width);
     p.teams = sru::cache::kMaxWarps / p.tw;
     p.blocks = (int)((Hq / Hkv + 7) / 8);
+    // a ring of 24 KB per warp, 32 KB for up to six warps
+    p.units = (p.tw * p.teams <= 6 ? 4 : 3) * (D <= 64 || p.width == 64 ? 2 : 1);
     // two pieces per CTA, a slice per warp for pieces that end early
     const size_t ctas = (size_t)sm_count();
     p.flags_off = round256((ctas * 2 * sru::cache::piece_floats(p.tw) +
@@ -2117,6 +2122,7 @@ sru_status sru_attention_decode(const void* q, const void* k_cache, const void* 
     a.ps = (int)page_size; a.maxp = (int)max_pages; a.pages = (int)pages;
     a.window = (int)std::min<int64_t>(window, INT32_MAX);
     a.out_f32 = out_t == SRU_F32;
+    a.width = (int)(max_pages * page_size);
     a.group = (int)(Hq / Hkv);
     a.blocks = p.blocks; a.tw = p.tw; a.teams = p.teams;
     a.box_rows = (int)std::min<int64_t>(page_size & -page_size, sru::cache::kStep);
@@ -2125,21 +2131,27 @@ sru_status sru_attention_decode(const void* q, const void* k_cache, const void* 
     const int threads = p.tw * p.teams * 32;
     // the rings, and room for the pieces that end early where it is left (the static part is
     // the scores' exchange, which a team of one warp does not have)
-    const size_t rings = (size_t)p.tw * p.teams * sru::cache::kRingBytes + 1024;
+    a.units = p.units;
+    const size_t unit = (D <= 64 || p.width == 64 ? 1 : 2) * sru::cache::kHalfBytes;
+    const size_t rings = (size_t)p.tw * p.teams * p.units * unit + 1024;
     const size_t early = (size_t)p.tw * p.teams * std::min<int64_t>(8, a.group) * sru::cache::kSlice * sizeof(float);
-    const size_t most = (size_t)(D == 128 ? 225 : 208) * 1024;
+    const size_t most = (size_t)(D == 128 ? 225 : D == 64 ? 224 : 207) * 1024;
     const bool fits = rings + early <= most;
     const size_t smem = rings + (fits ? early : 0);
     a.early_floats = fits ? (int)(early / sizeof(float)) / (p.tw * p.teams) : 0;
-    // D = 128, 256, 512, 1024: the forms without loops over the width
-    auto kern = D == 128   ? sru::cache::cache_attention_kernel<1>
-                : D == 256 ? sru::cache::cache_attention_kernel<2>
-                : D == 512 ? sru::cache::cache_attention_kernel<4>
-                : D == 1024 ? sru::cache::cache_attention_kernel<8>
-                            : sru::cache::cache_attention_kernel<0>;
+    using sru::cache::cache_attention_kernel;
+    auto kern = cache_attention_kernel<0, 0>;  // any D
+    switch (D) {                               // the forms without loops over the width
+        case 64: kern = cache_attention_kernel<1, 64>; break;
+        case 128: kern = cache_attention_kernel<1, 128>; break;
+        case 256: kern = cache_attention_kernel<2, 128>; break;
+        case 384: kern = cache_attention_kernel<3, 128>; break;
+        case 512: kern = cache_attention_kernel<4, 128>; break;
+        case 768: kern = cache_attention_kernel<6, 128>; break;
+        case 1024: kern = cache_attention_kernel<8, 128>; break;
+        default: break;
+    }
     SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kern), most));
-    // a wide team's pieces cost more to join than a few more steps of one team
-    a.min_steps = std::max(1, p.tw / 2);
     // The caches as (D, page_size, pages * Hkv), in boxes of 64 features x box_rows rows of
     // one page; for D a multiple of 64 as (64, page_size, D / 64, pages * Hkv), so that one
     // box holds a warp's 128 features.  Without pages nothing is loaded through the maps.
@@ -2150,7 +2162,7 @@ sru_status sru_attention_decode(const void* q, const void* k_cache, const void* 
         const uint64_t dims3[3] = {(uint64_t)D, (uint64_t)page_size, heads}, strides3[2] = {row, page};
         const uint64_t dims4[4] = {64, (uint64_t)page_size, (uint64_t)D / 64, heads}, strides4[3] = {row, 128, page};
         const uint32_t box3[3] = {64, (uint32_t)a.box_rows, 1};
-        const uint32_t box4[4] = {64, (uint32_t)a.box_rows, D > 64 ? 2u : 1u, 1};
+        const uint32_t box4[4] = {64, (uint32_t)a.box_rows, (uint32_t)(unit / sru::cache::kHalfBytes), 1};
         for (int i = 0; i < 2; ++i)
             if (!make_map(i ? &mv : &mk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.merged ? 4 : 3, i ? v_cache : k_cache,
                           a.merged ? dims4 : dims3, a.merged ? strides4 : strides3, a.merged ? box4 : box3,

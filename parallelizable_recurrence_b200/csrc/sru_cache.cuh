@@ -62,6 +62,33 @@ __device__ __forceinline__ unsigned long long block_inclusive(unsigned long long
     return v + (warp == 0 ? 0ull : before);
 }
 
+// The n (per lane) items of a warp's lanes, shared out evenly over the lanes, four at a
+// time each: store(src, i, load(src, i)) for item i of lane src.
+template <typename Load, typename Store>
+__device__ __forceinline__ void warp_spread(int n, Load load, Store store) {
+    const int lane = threadIdx.x & 31;
+    const int upto = (int)warp_inclusive((unsigned long long)n, lane);
+    const int total = __shfl_sync(0xffffffffu, upto, 31);
+    for (int b = 0; b < total; b += 128) {
+        int src[4], i[4], v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int e = b + k * 32 + lane;
+            src[k] = 0;  // the first lane whose running sum passes e
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                if (__shfl_sync(0xffffffffu, upto, src[k] + o - 1) <= e) src[k] += o;
+            const int before = __shfl_sync(0xffffffffu, upto - n, src[k]);
+            const int items = __shfl_sync(0xffffffffu, n, src[k]);
+            i[k] = e - before;
+            if (e >= total || i[k] >= items) i[k] = -1;
+            v[k] = load(src[k], i[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) store(src[k], i[k], v[k]);
+    }
+}
+
 __global__ void __launch_bounds__(kExtThreads) cache_extend_kernel(ExtendArgs a) {
     __shared__ unsigned long long sums[kExtThreads / 32];
     __shared__ int s_refused, s_taken;
@@ -89,13 +116,13 @@ __global__ void __launch_bounds__(kExtThreads) cache_extend_kernel(ExtendArgs a)
         const int gone = add < 0 ? held : 0;
         upto = block_inclusive((unsigned)max(add, 0) | (unsigned long long)gone << 32, sums, total);
         const int base = n_free + gone_before + (int)(upto >> 32) - gone;
-        for (unsigned left = __ballot_sync(0xffffffffu, gone > 0); left != 0; left &= left - 1) {
-            const int src = __ffs(left) - 1;
-            const int n = __shfl_sync(0xffffffffu, gone, src), at = __shfl_sync(0xffffffffu, base, src);
-            const int* row = a.table + (size_t)(b0 + tid - lane + src) * a.maxp;
-            for (int i = lane; i < n; i += 32)
-                if (at + i >= 0 && at + i < a.pages) a.free_pages[at + i] = row[i];
-        }
+        const int warp_b = b0 + tid - lane;
+        warp_spread(
+            gone, [&](int src, int i) { return i >= 0 ? a.table[(size_t)(warp_b + src) * a.maxp + i] : 0; },
+            [&](int src, int i, int page) {
+                const int at = __shfl_sync(0xffffffffu, base, src) + i;
+                if (i >= 0 && at >= 0 && at < a.pages) a.free_pages[at] = page;
+            });
         gone_before += (int)(total >> 32);
     }
     __syncthreads();
@@ -128,16 +155,17 @@ __global__ void __launch_bounds__(kExtThreads) cache_extend_kernel(ExtendArgs a)
         // page p >= held of this request is stack entry top - p
         const int top = avail - 1 - (wanted - need) + held, take = ok ? need : 0;
         int* row = a.table + (size_t)b * a.maxp;
-        if (take <= 2) {
-            for (int i = 0; i < take; ++i) row[held + i] = stack(top - held - i);
-        }
-        for (unsigned left = __ballot_sync(0xffffffffu, take > 2); left != 0; left &= left - 1) {
-            const int src = __ffs(left) - 1;
-            const int n = __shfl_sync(0xffffffffu, take, src), at = __shfl_sync(0xffffffffu, held, src);
-            const int from = __shfl_sync(0xffffffffu, top, src);
-            int* r = a.table + (size_t)(b0 + tid - lane + src) * a.maxp;
-            for (int i = at + lane; i < at + n; i += 32) r[i] = stack(from - i);
-        }
+        const int warp_b = b0 + tid - lane;
+        warp_spread(
+            take,
+            [&](int src, int i) {
+                const int p = __shfl_sync(0xffffffffu, held, src) + i, from = __shfl_sync(0xffffffffu, top, src);
+                return i >= 0 ? stack(from - p) : 0;
+            },
+            [&](int src, int i, int page) {
+                const int p = __shfl_sync(0xffffffffu, held, src) + i;
+                if (i >= 0) a.table[(size_t)(warp_b + src) * a.maxp + p] = page;
+            });
         // slot of token j of a request
         auto slot = [&](const int* r, int len_, int held_, int top_, int j) {
             const int pos = len_ + j, p = pos / a.ps;
@@ -151,17 +179,19 @@ __global__ void __launch_bounds__(kExtThreads) cache_extend_kernel(ExtendArgs a)
                 if (first + j < (unsigned)a.T) a.slots[first + j] = ok ? slot(row, len, held, top, j) : -1;
         }
         if (!a.rows_kernel) {
-            for (unsigned left = __ballot_sync(0xffffffffu, grow > kExtDirect && first < (unsigned)a.T); left != 0;
-                 left &= left - 1) {
-                const int src = __ffs(left) - 1;
-                const int n = __shfl_sync(0xffffffffu, grow, src), at = __shfl_sync(0xffffffffu, (int)first, src);
-                const int len_ = __shfl_sync(0xffffffffu, len, src), held_ = __shfl_sync(0xffffffffu, held, src);
-                const int top_ = __shfl_sync(0xffffffffu, top, src);
-                const bool ok_ = __shfl_sync(0xffffffffu, (int)ok, src) != 0;
-                const int* r = a.table + (size_t)(b0 + tid - lane + src) * a.maxp;
-                const int rows = min(n, a.T - at);
-                for (int j = lane; j < rows; j += 32) a.slots[at + j] = ok_ ? slot(r, len_, held_, top_, j) : -1;
-            }
+            const int rows = grow > kExtDirect && first < (unsigned)a.T ? min(grow, a.T - (int)first) : 0;
+            warp_spread(
+                rows,
+                [&](int src, int i) {
+                    const int len_ = __shfl_sync(0xffffffffu, len, src), held_ = __shfl_sync(0xffffffffu, held, src);
+                    const int top_ = __shfl_sync(0xffffffffu, top, src);
+                    const bool ok_ = __shfl_sync(0xffffffffu, (int)ok, src) != 0;
+                    return i >= 0 && ok_ ? slot(a.table + (size_t)(warp_b + src) * a.maxp, len_, held_, top_, i) : -1;
+                },
+                [&](int src, int i, int s) {
+                    const int at = (int)__shfl_sync(0xffffffffu, first, src);
+                    if (i >= 0) a.slots[at + i] = s;
+                });
         }
         if (b < a.B) {
             a.lengths_out[b] = add < 0 ? 0 : (ok ? (int)end : len);

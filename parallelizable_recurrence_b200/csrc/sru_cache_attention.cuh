@@ -17,9 +17,9 @@
 // finish joins theirs through the workspace, in the order of the keys whoever that
 // is.  (A second kernel for it cost 5 to 9 us.)
 //
-// A team is TW = ceil(D / 128) warps; warp w owns features 128 w .. of q, k, v and
-// o.  It loads its part itself, by TMA: units of 32 rows x 128 features through a
-// ring of three whose barriers no other warp touches.  A page of ps tokens allows
+// A team is TW = ceil(D / W) warps, W = 128 (or 64) features; warp w owns features
+// W w .. of q, k, v and o.  It loads its part itself, by TMA: units of 32 rows x W
+// features through a ring whose barriers no other warp touches.  A page of ps tokens allows
 // boxes of R rows, R the largest power of two (<= 32) that divides ps.  Keys are
 // rows of the tensor-core products -- S^T = K Q^T (16 keys x 8 heads), O^T = V^T P^T
 // (16 features x 8 heads) -- so a group of up to 8 heads costs what one does, and
@@ -36,11 +36,11 @@ namespace sru {
 namespace cache {
 
 constexpr int kStep = 32;     // keys per step
-constexpr int kSlice = 128;   // features per warp
+constexpr int kSlice = 128;   // most features per warp
 constexpr int kMaxWarps = 8;  // per CTA
-constexpr uint32_t kHalfBytes = kStep * 128;       // 64 features of a step's rows
-constexpr uint32_t kRingBytes = 6 * kHalfBytes;    // per warp: 3 units, or 6 of one half when D <= 64
-constexpr int kMasks = 4;     // steps whose keys' mask is held
+constexpr uint32_t kHalfBytes = kStep * 128;        // 64 features of a step's rows
+constexpr uint32_t kRingBytes = 8 * kHalfBytes;     // per warp, at most
+constexpr int kMasks = 8;     // steps whose keys' mask is held
 
 struct DecodeArgs {
     const __nv_bfloat16 *q, *k, *v;
@@ -51,12 +51,13 @@ struct DecodeArgs {
     unsigned long long* flags;   // the same index: the CTA's piece is there, if equal to
     unsigned long long tag;      // this call's number
     int B, Hq, Hkv, D, ps, maxp, pages, window, out_f32;
+    int width;           // keys that the table has room for
     int group;           // query heads per key head
     int blocks;          // head blocks per key head
     int tw, teams;       // warps per team, teams per CTA
     int box_rows;        // R
     int merged;          // the maps are 4-D and one box holds both halves of a unit's rows
-    int min_steps;       // per team
+    int units;           // of a warp's ring
     int early_floats;    // shared floats per warp for a piece that ends before its team's range; 0: workspace
     float scale_log2;    // scale * log2 e
 };
@@ -102,18 +103,17 @@ __device__ __forceinline__ void team_sync(int team, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
 }
 
-// First key, one past the last key, and first step of a request; steps() = 0 when empty.
+// First key, one past the last key, and first step of a request; s1 <= s0 when empty.
 struct Span {
     int lo, hi, s0, s1;
-    __device__ int steps() const { return s1 - s0; }
+    __device__ int steps() const { return max(s1 - s0, 0); }
 };
 __device__ __forceinline__ Span span_of(const DecodeArgs& a, int b) {
     Span x;
-    const long long width = (long long)a.maxp * a.ps;
-    x.hi = (int)min((long long)max(a.lengths[b], 0), width);
+    x.hi = min(max(a.lengths[b], 0), a.width);
     x.lo = a.window > 0 ? max(0, x.hi - a.window) : 0;
     x.s0 = x.lo / kStep;
-    x.s1 = (x.hi + kStep - 1) / kStep;
+    x.s1 = (int)(((unsigned)x.hi + kStep - 1) / kStep);
     return x;
 }
 
@@ -134,37 +134,40 @@ struct Cursor {
     }
 };
 
-// A run of pieces of one item, found from the CTA's (or the CTAs') bookkeeping.
+// An item that is in pieces: its place, and its steps in the list.
 struct Item {
-    int b, hh;
-    long long first, last;  // its steps in the list
+    int b, hh, first, last;
 };
-
-// TW = 0: any number of warps per team and any width; otherwise TW warps of 128 features
-// each (D = 128 TW), which makes the loops over features and warps straight code.
-template <int TW>
+// TW, W > 0: TW warps of W features each (D = TW W, W = 64 or 128), which makes the loops
+// over features and warps straight code.  TW = W = 0: any D.
+template <int TW, int W>
 __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     cache_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                            const __grid_constant__ DecodeArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ float4 exch[2][kMaxWarps][2][32];
-    constexpr int kMaxUnits = TW > 0 ? 3 : 6;
-    __shared__ uint64_t s_full[kMaxWarps][kMaxUnits];
+    constexpr int kWidth = W > 0 ? W : kSlice;             // features per warp
+    constexpr int kUnits = W == 64 || W == 0 ? 8 : 4;      // most units of a ring
+    constexpr bool kExch = TW != 1;
+    __shared__ float4 exch[kExch ? 2 : 1][kExch ? kMaxWarps : 1][kExch ? 2 : 1][kExch ? 32 : 1];
+    __shared__ uint64_t s_full[kMaxWarps][kUnits];
     __shared__ uint32_t s_mask[kMaxWarps][kMasks];
-    __shared__ long long s_scan[kMaxWarps], s_rem[kMaxWarps];
-    __shared__ int s_b[kMaxWarps];
-    // pieces of each team: [0] goes on with an item (1: and not to its end, 2: to its end), [1] starts one
-    __shared__ int s_has[kMaxWarps][2], s_end[kMaxWarps];  // s_end: [0] is the range's last step
+    __shared__ long long s_sum[kMaxWarps];
+    __shared__ int s_most[kMaxWarps];
+    // pieces of each team: [0] goes on with an item (1: and not to its end, 2: to its end), [1] starts
+    // one; s_end: [0] is the range's last step
+    __shared__ int s_has[kMaxWarps][2], s_end[kMaxWarps];
     __shared__ Item s_item[kMaxWarps][2];
-    __shared__ float s_ml[kMaxWarps][2][16];   // their m and l
+    __shared__ float s_ml[kMaxWarps][2][16];  // their m and l
+    static_assert(sizeof(s_ml) >= kMaxWarps * 32 * sizeof(int), "also holds an int per thread");
+    int* s_before = reinterpret_cast<int*>(s_ml);
     __shared__ int s_last[2];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthreads = blockDim.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthreads = blockDim.x, n_warps = nthreads >> 5;
     const int HH = a.Hkv * a.blocks;
     const int tw = TW > 0 ? TW : a.tw, teams = TW > 0 ? kMaxWarps / TW : a.teams;
 
     if (lane == 0) {
-        for (int i = 0; i < kMaxUnits; ++i) mbar_init(&s_full[warp][i], 1);
+        for (int i = 0; i < kUnits; ++i) mbar_init(&s_full[warp][i], 1);
         fence_mbar_init();
         s_has[warp][0] = s_has[warp][1] = 0;
     }
@@ -177,9 +180,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     // ---- this CTA's teams' places in the list: sums of steps over the requests
     const int per_thread = (a.B + nthreads - 1) / nthreads;
     long long mine = 0;
-    for (int i = 0; i < per_thread; ++i) {
-        const int b = tid * per_thread + i;
-        if (b < a.B) mine += (long long)max(span_of(a, b).steps(), 0) * HH;
+    int longest = 0;
+#pragma unroll 1
+    for (int b = tid * per_thread; b < min(a.B, (tid + 1) * per_thread); ++b) {
+        const int n = span_of(a, b).steps();
+        mine += (long long)n * HH;
+        longest = max(longest, n);
     }
     long long upto = mine;
 #pragma unroll
@@ -187,63 +193,70 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         const long long u = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += u;
     }
-    if (lane == 31) s_scan[warp] = upto;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 31) {
+        s_sum[warp] = upto;
+        s_most[warp] = longest;
+    }
     __syncthreads();
-    long long total = 0, before = upto - mine;
-    for (int w = 0; w < nthreads / 32; ++w) {
-        if (w < warp) before += s_scan[w];
-        total += s_scan[w];
+    long long total64 = 0, before = upto - mine;
+#pragma unroll 1
+    for (int w = 0; w < n_warps; ++w) {
+        if (w < warp) before += s_sum[w];
+        total64 += s_sum[w];
+        longest = max(longest, s_most[w]);
     }
-    const long long n_teams = (long long)gridDim.x * teams;
-    const long long per = max((long long)a.min_steps, (total + n_teams - 1) / n_teams);
-    for (int t = 0; t < teams; ++t) {
-        const long long g0 = ((long long)blockIdx.x * teams + t) * per;
-        if (g0 >= before && g0 < before + mine) {
-            long long at = before;
-            for (int b = tid * per_thread;; ++b) {
-                const long long n = (long long)max(span_of(a, b).steps(), 0) * HH;
-                if (g0 < at + n) {
-                    s_b[t] = b;
-                    s_rem[t] = g0 - at;
-                    break;
-                }
-                at += n;
-            }
-        }
+    if (total64 >= 1 << 30) {  // (places in the list are counted in 32 bits)
+        if (tid == 0) record_error(kErrBadIndex);
+        return;
     }
+    const int total = (int)total64;
+    // steps per team; at most about 64 CTAs share an item, whose pieces one of them joins
+    const int n_teams = gridDim.x * teams;
+    const int per = max(max((total + n_teams - 1) / n_teams, (longest + 64 * teams - 1) / (64 * teams)), 1);
+    s_before[tid] = (int)before;
     __syncthreads();
 
     auto heads_of = [&](int hh) { return min(8, a.group - hh % a.blocks * 8); };
     auto head0_of = [&](int hh) { return hh / a.blocks * a.group + hh % a.blocks * 8; };
     const int team = warp / tw, w_in = warp - team * tw;
-    const long long my_team = (long long)blockIdx.x * teams + team;
-    const long long g0 = my_team * per, g1 = min(total, g0 + per);
-    const int n_steps = g0 < g1 ? (int)(g1 - g0) : 0;
-
-    uint8_t* ring = smem + warp * kRingBytes;
-    // a piece that ends within the range: behind the rings, or in the workspace
-    float* early = a.early_floats > 0
-                       ? reinterpret_cast<float*>(smem + tw * teams * kRingBytes) + (size_t)warp * a.early_floats
-                       : a.part + (size_t)gridDim.x * 2 * piece_floats(tw) +
-                             ((size_t)blockIdx.x * kMaxWarps + warp) * kSliceFloats;
-    if (n_steps > 0) {
+    const int my_team = blockIdx.x * teams + team;
+    const int g0 = my_team * per, g1 = min(total, g0 + per);
+    const int n_steps = max(g1 - g0, 0);
     Cursor cur;
-    {
-        cur.b = s_b[team];
-        cur.sp = span_of(a, cur.b);
-        const int n = cur.sp.steps();
-        cur.hh = (int)(s_rem[team] / n);
-        cur.s = cur.sp.s0 + (int)(s_rem[team] - (long long)cur.hh * n);
+    if (n_steps > 0) {
+        int t = 0;  // the last thread whose requests start at or before g0 (nthreads <= 256)
+#pragma unroll
+        for (int o = kMaxWarps * 16; o > 0; o >>= 1)
+            if (t + o < nthreads && s_before[t + o] <= g0) t += o;
+        int at = s_before[t], n;
+        cur.b = t * per_thread;
+        while (g0 >= at + (n = (cur.sp = span_of(a, cur.b)).steps()) * HH) {
+            at += n * HH;
+            ++cur.b;
+        }
+        cur.hh = (g0 - at) / n;
+        cur.s = cur.sp.s0 + (g0 - at) - cur.hh * n;
     }
-    const int f0 = w_in * kSlice;                                   // first feature of this warp
-    const int width = TW > 0 ? kSlice : min(kSlice, a.D - f0);      // its features, a multiple of 8
-    const int n_units = TW > 0 || a.D > 64 ? 3 : 6, halves = TW > 0 || a.D > 64 ? 2 : 1;
+    __syncthreads();  // s_before has been read: s_ml may be written
+    const int n_units = a.units;
+    const uint32_t ring_bytes = n_units * (W == 64 || (W == 0 && a.D <= 64) ? kHalfBytes : 2 * kHalfBytes);
+    uint8_t* ring = smem + warp * ring_bytes;
+    // pieces that end within the range lie behind the rings, or in the workspace
+    const int early_stride = a.early_floats > 0 ? a.early_floats : kSliceFloats;
+    float* early0 = a.early_floats > 0 ? reinterpret_cast<float*>(smem + n_warps * ring_bytes)
+                                       : a.part + (size_t)gridDim.x * 2 * piece_floats(tw) +
+                                             (size_t)blockIdx.x * kMaxWarps * kSliceFloats;
+    if (n_steps > 0) {
+    const int f0 = w_in * kWidth;                                   // first feature of this warp
+    const int width = W > 0 ? W : min(kSlice, a.D - f0);            // its features, a multiple of 8
+    const int halves = W > 0 ? W / 64 : (a.D > 64 ? 2 : 1);         // boxes of 64 features per row group
     const uint32_t unit_bytes = halves * kHalfBytes;
 
     // ---- loads.  Lane l has the box of row group l; units come in the order of use: K of step
     // 0, then K of step j + 1 and V of step j, at last V of the last step.
     const int R = a.box_rows, groups = kStep / R;
-    const int boxes = a.merged ? 1 : (width > 64 ? 2 : 1);          // per group
+    const int boxes = a.merged ? 1 : (width > 64 ? 2 : 1);
     const uint32_t box_bytes = R * 128 * (a.merged ? halves : 1);
     Cursor ld = cur;
     int next_page = 0, next_in = -1;  // table entry of this lane's box of step `ld`; < 0: no key of it is wanted
@@ -330,8 +343,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     };
 
     const int g = lane >> 2, t2 = (lane & 3) * 2;
-    uint32_t qf[kSlice / 16][2];
-    float o[kSlice / 16][4];
+    uint32_t qf[kWidth / 16][2];
+    float o[kWidth / 16][4];
     float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;  // heads t2, t2 + 1
     float sc[2][4];                                // scores: keys 16 i + g and + 8, heads t2 and t2 + 1
     uint32_t ph[2][2], pl[2][2], mask = 0;
@@ -348,7 +361,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                 const int heads = heads_of(nxt.hh);
                 const __nv_bfloat16* q = a.q + ((size_t)nxt.b * a.Hq + head0_of(nxt.hh) + min(g, heads - 1)) * a.D + f0;
 #pragma unroll
-                for (int kk = 0; kk < kSlice / 16; ++kk) {
+                for (int kk = 0; kk < kWidth / 16; ++kk) {
                     const int x = kk * 16 + t2;
                     qf[kk][0] = g < heads && x < width ? *reinterpret_cast<const uint32_t*>(q + x) : 0u;
                     qf[kk][1] = g < heads && x + 8 < width ? *reinterpret_cast<const uint32_t*>(q + x + 8) : 0u;
@@ -358,8 +371,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
 #pragma unroll
-            for (int kk = 0; kk < kSlice / 16; ++kk) {
-                if (TW == 0 && kk * 16 >= width) break;
+            for (int kk = 0; kk < kWidth / 16; ++kk) {
+                if (W == 0 && kk * 16 >= width) break;
                 const uint32_t at = base + (kk >> 2) * half_at + (((2 * (kk & 3) + k_hi) ^ k_x[kk >> 2]) << 4);
                 uint32_t ka[4], kb[4];
                 ldsm4(at, ka);
@@ -384,8 +397,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             }
             const uint32_t base = unit + v_at;
 #pragma unroll
-            for (int mt = 0; mt < kSlice / 16; ++mt) {
-                if (TW == 0 && mt * 16 >= width) break;
+            for (int mt = 0; mt < kWidth / 16; ++mt) {
+                if (W == 0 && mt * 16 >= width) break;
                 const uint32_t at = base + (mt >> 2) * half_at + (((2 * (mt & 3) + v_hi) ^ v_x[mt >> 2]) << 4);
                 uint32_t va[4], vb[4];
                 ldsm4_t(at, va);
@@ -410,9 +423,9 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                 const float r1 = whole ? (s1 > 0.f ? 1.f / s1 : 0.f) : 1.f;
                 const int kind = begins ? 1 : 0;
                 // the last piece of the range may lie in the ring, which is idle then
-                float* part = !more ? reinterpret_cast<float*>(ring) : early;
+                float* part = !more ? reinterpret_cast<float*>(ring) : early0 + warp * early_stride;
 #pragma unroll
-                for (int mt = 0; mt < kSlice / 16; ++mt) {
+                for (int mt = 0; mt < kWidth / 16; ++mt) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int head = t2 + (e & 1), x = mt * 16 + g + (e >> 1) * 8;
@@ -445,8 +458,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                 if (!whole && w_in == 0 && lane == 0) {
                     s_has[team][kind] = ends ? 2 : 1;
                     if (kind == 0) s_end[team] = !more;
-                    s_item[team][kind] = Item{cur.b, cur.hh, g0 + step - (cur.s - cur.sp.s0),
-                                              g0 + step + (cur.sp.s1 - 1 - cur.s)};
+                    s_item[team][kind] =
+                        Item{cur.b, cur.hh, g0 + step - (cur.s - cur.sp.s0), g0 + step + (cur.sp.s1 - 1 - cur.s)};
                 }
                 begins = true;  // (the next step, if any, starts an item)
             }
@@ -454,7 +467,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         if (!more) break;
         cur = nxt;
         // ---- whole scores from the team's parts
-        if (TW != 1 && tw > 1) {
+        if (kExch && tw > 1) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) exch[buf][warp][i][lane] = make_float4(sc[i][0], sc[i][1], sc[i][2], sc[i][3]);
             team_sync(team, tw * 32);
@@ -482,7 +495,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             m0 = m1 = -INFINITY;
             l0 = l1 = 0.f;
 #pragma unroll
-            for (int mt = 0; mt < kSlice / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+            for (int mt = 0; mt < kWidth / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
         }
         mask = s_mask[warp][(step + 1) & (kMasks - 1)];
         float n0 = m0, n1 = m1;
@@ -511,7 +524,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             l0 *= f0c;
             l1 *= f1c;
 #pragma unroll
-            for (int mt = 0; mt < kSlice / 16; ++mt) {
+            for (int mt = 0; mt < kWidth / 16; ++mt) {
                 o[mt][0] *= f0c;
                 o[mt][1] *= f1c;
                 o[mt][2] *= f0c;
@@ -547,10 +560,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     }  // n_steps > 0
 
     // requests without keys: their output is zero
+#pragma unroll 1
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        const Span sp = span_of(a, b);
-        if (tid == 0 && a.lengths[b] > sp.hi) record_error(kErrBadIndex);  // longer than the table is wide
-        if (sp.steps() > 0) continue;
+        const int len = a.lengths[b];
+        if (tid == 0 && len > a.width) record_error(kErrBadIndex);  // longer than the table is wide
+        if (len > 0 && a.width > 0) continue;
+#pragma unroll 1
         for (int i = tid; i < a.Hq * a.D; i += nthreads) {
             const size_t at = (size_t)b * a.Hq * a.D + i;
             if (a.out_f32) static_cast<float*>(a.out)[at] = 0.f;
@@ -559,11 +574,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         if (a.lse != nullptr)
             for (int i = tid; i < a.Hq; i += nthreads) a.lse[(size_t)b * a.Hq + i] = -INFINITY;
     }
-    if ((long long)blockIdx.x * teams * per >= total) return;  // no steps for this CTA
+    if (blockIdx.x * teams * per >= total) return;  // no steps for this CTA
 
     // ---- joining.  One head and 128 features of n pieces per warp, a lane four features:
     // unnormalised sum, m and l; load_o(i) gives piece i's four features, load_ml(i, j) its m and l.
-    const int n_warps = nthreads >> 5;
     auto join = [&](int n, auto load_o, auto load_ml, float4& acc, float& top, float& l) {
         constexpr int kAhead = 8;
         top = -INFINITY;
@@ -607,8 +621,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     auto store = [&](const Item& it, int head, int slice, const float4& acc, float top, float l) {
         const float r = l > 0.f ? 1.f / l : 0.f;
         const size_t row = (size_t)it.b * a.Hq + head0_of(it.hh) + head;
-        const int c = slice * kSlice + lane * 4;
-        if (c < a.D) {
+        const int c = slice * kWidth + lane * 4;
+        if (lane * 4 < kWidth && c < a.D) {
             if (a.out_f32)
                 *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * a.D + c) =
                     make_float4(acc.x * r, acc.y * r, acc.z * r, acc.w * r);
@@ -643,9 +657,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             auto load_o = [&](int i) {
                 const int w = (from + i) * tw + slice;
                 const bool in_ring = (i == 0 && kind == 1) || s_end[from + i];
-                const float* o_p = in_ring ? reinterpret_cast<const float*>(smem + w * kRingBytes)
-                                           : early + ((long long)w - warp) *
-                                                         (a.early_floats > 0 ? a.early_floats : kSliceFloats);
+                const float* o_p = in_ring ? reinterpret_cast<const float*>(smem + w * ring_bytes)
+                                           : early0 + w * early_stride;
                 return reinterpret_cast<const float4*>(o_p + head * kSlice)[lane];
             };
             auto load_ml = [&](int i, int j) { return s_ml[from + i][i == 0 ? kind : 0][j + head]; };
@@ -678,7 +691,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     // across CTAs: each raises the flag of its piece, then looks at the flags of all pieces of
     // the item.  The last to raise one sees them all and joins them (so may another that
     // looks later: it writes the same), and lowers the flags for a replay of this call.
-    const long long cta_steps = per * teams;
+    const int cta_steps = per * teams;
     __syncthreads();
     if (tid == 0) {
         __threadfence();  // this CTA's pieces before their flags
@@ -692,7 +705,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         if (warp != (kind == 1 || n_warps == 1 ? 0 : 1)) continue;
         bool all = kind ? has_out : has_in;
         const Item it = kind ? out_item : in_item;
-        const int c0 = (int)(it.first / cta_steps), n = all ? (int)(it.last / cta_steps) - c0 + 1 : 0;
+        const int c0 = it.first / cta_steps, n = all ? it.last / cta_steps - c0 + 1 : 0;
         for (int i = lane; i < n; i += 32)
             all = all && *reinterpret_cast<volatile unsigned long long*>(
                              a.flags + (size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) == a.tag;
@@ -705,7 +718,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     for (int kind = 1; kind >= 0; --kind) {
         if (!s_last[kind]) continue;
         const Item it = kind ? out_item : in_item;
-        const int c0 = (int)(it.first / cta_steps), n = (int)(it.last / cta_steps) - c0 + 1;
+        const int c0 = it.first / cta_steps, n = it.last / cta_steps - c0 + 1;
         auto index = [&](int i) { return (size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0); };
         const int tasks = heads_of(it.hh) * tw;
         for (int q = (warp - turn % n_warps + n_warps) % n_warps; q < tasks; q += n_warps) {
