@@ -319,14 +319,12 @@ constexpr uint32_t kGemmBRows = (uint32_t)sru::gemm::P_CN;
 // tail_split (pair kernel, OUT == kOutF32 only): the output tiles of the last,
 // partial round of CTA pairs are cut in two k-pieces that add onto regions
 // zeroed here first (see sru::gemm::pair_next).
-// CHAIN: an overlapped launch whose output is multiplied by *scale (device memory).
-template <bool A_MN, bool B_MN, int OUT, bool CHAIN = false>
+template <bool A_MN, bool B_MN, int OUT>
 sru_status launch_tc_gemm(const CUtensorMap& ma, const CUtensorMap& mb, void* out, int64_t R, int64_t C,
-                          int64_t Kr, cudaStream_t st, int splits = 1, int64_t ldo = -1, bool tail_split = false,
-                          const float* scale = nullptr) {
+                          int64_t Kr, cudaStream_t st, int splits = 1, int64_t ldo = -1, bool tail_split = false) {
     if (ldo < 0) ldo = C;
     {
-        auto kern = sru::gemm::tc_gemm_pair_kernel<A_MN, B_MN, OUT, 0, 0, 0, 0, CHAIN>;
+        auto kern = sru::gemm::tc_gemm_pair_kernel<A_MN, B_MN, OUT>;
         SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kern), sru::gemm::P_SMEM_BYTES));
         // the output as the epilogue's TMA store target: boxes of 32 rows x 128 bytes
         // (64 bf16 or 32 fp32 columns), swizzled like the staging buffers
@@ -362,11 +360,8 @@ sru_status launch_tc_gemm(const CUtensorMap& ma, const CUtensorMap& mb, void* ou
                                                                    (long long)ldo, (int)n_tiles, (int)(F * pairs));
             SRU_CUDA_TRY(cudaGetLastError());
         }
-        if (CHAIN)
-            return launch_overlapped(kern, dim3((unsigned)(2 * pairs)), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st,
-                                     ma, mb, mo, (int)R, (int)C, (int)Kr, splits, 1, tail_s, 0, scale);
         kern<<<(unsigned)(2 * pairs), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st>>>(
-            ma, mb, mo, (int)R, (int)C, (int)Kr, splits, 1, tail_s, 0, nullptr);
+            ma, mb, mo, (int)R, (int)C, (int)Kr, splits, 1, tail_s, 0);
     }
     SRU_CUDA_TRY(cudaGetLastError());
     return SRU_OK;
@@ -411,7 +406,7 @@ sru_status launch_batched_bpo(const CUtensorMap& ma, const CUtensorMap& mb, void
             return SRU_ERR_INVALID;
     }
     kern<<<(unsigned)(2 * pairs), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st>>>(
-        ma, mb, mo, (int)R, (int)C, (int)Kr, 1, (int)batches, 0, 0, nullptr);
+        ma, mb, mo, (int)R, (int)C, (int)Kr, 1, (int)batches, 0, 0);
     SRU_CUDA_TRY(cudaGetLastError());
     return SRU_OK;
 }
@@ -1348,7 +1343,7 @@ static sru_status project_dW_split(const void* dU, const void* X, float* dW, int
     const int64_t units = tiles * pl.splits;
     const int64_t pairs = units < sm_count() / 2 ? units : sm_count() / 2;
     kern<<<(unsigned)(2 * pairs), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st>>>(
-        ma, mb, mo, (int)N, (int)K, (int)M, (int)pl.splits, 1, 0, (int)pl.slab_rows, nullptr);
+        ma, mb, mo, (int)N, (int)K, (int)M, (int)pl.splits, 1, 0, (int)pl.slab_rows);
     SRU_CUDA_TRY(cudaGetLastError());
     const size_t n4 = (size_t)N * K / 4;
     sru::gemm::splitk_reduce_kernel<<<(unsigned)std::min<size_t>(blocks_for(n4, 256), (size_t)sm_count() * 8), 256, 0,
@@ -1766,6 +1761,52 @@ struct LossPlan {
     SplitPlan dh, dw;
     size_t partial_off, target_off, scale_off, dz_off, dh_off, dw_off, forward_total, total;
 };
+// The gradient products of a piece share a launch (sru::loss::grad_unit deals the units).
+// A k-block costs 0.35 us (measured), a unit at least what its epilogue takes, 3 us.
+static double grad_unit_us(int64_t kblocks) { return std::max(kblocks * 0.35, 3.0) + 0.5; }
+// units of problem 1 that a pair takes while others have one more of problem 0
+static int64_t grad_extra(double t0, double t1) { return (int64_t)(t0 / t1); }
+// the time of the pair with the most to do
+static double grad_us(int64_t u0, double t0, int64_t u1, double t1, int64_t P) {
+    const int64_t r = u0 % P, e = r > 0 ? std::min(u1, grad_extra(t0, t1) * (P - r)) : 0, rest = u1 - e;
+    const double all = u0 / P * t0 + rest / P * t1;  // (whole rounds)
+    const double busy = r > 0 ? t0 + (rest % P > P - r ? t1 : 0.0) : 0.0;
+    const double others = (r > 0 ? (double)((e + P - r - 1) / (P - r)) * t1 : 0.0) + (rest % P > 0 ? t1 : 0.0);
+    return all + std::max(busy, others);
+}
+// The k parts of both products: the split with the least time, where slabs cost their
+// bytes twice at 5 TB/s and 3 us for their sum.
+static void grad_plan(int64_t M, int64_t n, int64_t K, LossPlan& p) {
+    const int64_t P = sm_count() / 2, bm = sru::gemm::P_BM, tn = (K + sru::gemm::P_BN - 1) / sru::gemm::P_BN;
+    const int64_t rows[2] = {M, n}, kb[2] = {(n + 63) / 64, (M + 63) / 64};
+    static const int64_t tries[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
+    SplitPlan* out[2] = {&p.dh, &p.dw};
+    double best = 1e30;
+    for (int64_t s0 : tries) {
+        for (int64_t s1 : tries) {
+            const int64_t want[2] = {s0, s1};
+            double slabs = 0.0, unit[2];
+            int64_t S[2], units[2];
+            bool fits = true;
+            for (int i = 0; i < 2; ++i) {
+                if (want[i] > 1 && want[i] * 4 > kb[i]) fits = false;
+                const int64_t per = (kb[i] + want[i] - 1) / want[i], mt = (rows[i] + bm - 1) / bm;
+                S[i] = (kb[i] + per - 1) / per;  // no part is empty
+                unit[i] = grad_unit_us(per);
+                units[i] = mt * tn * S[i];
+                if (S[i] > 1) slabs += (double)S[i] * mt * bm * K * 4 * 2 / 5.0e6 + 3.0;
+            }
+            const double t = grad_us(units[0], unit[0], units[1], unit[1], P) + slabs;
+            if (!fits || t >= best) continue;
+            best = t;
+            for (int i = 0; i < 2; ++i) {
+                out[i]->splits = S[i];
+                out[i]->slab_rows = (rows[i] + bm - 1) / bm * bm;
+                out[i]->bytes = S[i] > 1 ? (size_t)S[i] * out[i]->slab_rows * K * 4 : 0;
+            }
+        }
+    }
+}
 static LossPlan loss_plan(int64_t M, int64_t V, int64_t K, bool backward) {
     LossPlan p{};
     p.warps = K < kLossShortK ? 8 : 4;
@@ -1779,8 +1820,7 @@ static LossPlan loss_plan(int64_t M, int64_t V, int64_t K, bool backward) {
     const int64_t n = (V + most - 1) / most;
     p.Vc = ((V + n - 1) / n + sru::gemm::P_BN - 1) / sru::gemm::P_BN * sru::gemm::P_BN;
     p.pieces = (V + p.Vc - 1) / p.Vc;
-    p.dh = split_plan(M, K, std::min(p.Vc, V));
-    p.dw = split_plan(std::min(p.Vc, V), K, M);
+    grad_plan(M, std::min(p.Vc, V), K, p);
     p.dz_off = 256;  // behind the weights' scale
     p.dh_off = p.dz_off + round256((size_t)M * p.Vc * 2);
     p.dw_off = p.dh_off + round256(p.dh.splits > 1 ? p.dh.bytes : (p.pieces > 1 ? (size_t)M * K * 4 : 0));
@@ -1812,24 +1852,6 @@ static sru_status launch_vocab(int warps, const CUtensorMap& mh, const CUtensorM
                                const sru::loss::LossArgs& a, int64_t M, int64_t N, int64_t K, cudaStream_t st) {
     return warps == 8 ? launch_vocab_w<EPI, 8>(mh, mw, mdz, a, M, N, K, st)
                       : launch_vocab_w<EPI, 4>(mh, mw, mdz, a, M, N, K, st);
-}
-template <bool A_MN, bool B_MN, int OUT>
-static sru_status launch_slabs(const CUtensorMap& ma, const CUtensorMap& mb, void* slabs, int64_t R, int64_t C,
-                               int64_t Kr, int64_t splits, int64_t slab_rows, int64_t all_splits, const float* scale,
-                               cudaStream_t st) {
-    auto kern = sru::gemm::tc_gemm_pair_kernel<A_MN, B_MN, OUT, 0, 0, 0, 0, true>;
-    SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kern), sru::gemm::P_SMEM_BYTES));
-    CUtensorMap mo;
-    const uint64_t dims[2] = {(uint64_t)C, (uint64_t)(slab_rows * all_splits)};
-    const uint64_t strides[1] = {(uint64_t)C * 4};
-    const uint32_t box[2] = {(uint32_t)sru::gemm::EpiChunk<OUT>::kCols, 32};
-    if (!make_map(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, slabs, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
-        return SRU_ERR_INVALID;
-    const int64_t units =
-        ((R + sru::gemm::P_BM - 1) / sru::gemm::P_BM) * ((C + sru::gemm::P_BN - 1) / sru::gemm::P_BN) * splits;
-    const int64_t pairs = std::min<int64_t>(units, sm_count() / 2);
-    return launch_overlapped(kern, dim3((unsigned)(2 * pairs)), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st, ma, mb,
-                             mo, (int)R, (int)C, (int)Kr, (int)splits, 1, 0, (int)slab_rows, scale);
 }
 static sru_status sum_slabs(const void* slabs, void* out, int out_t, int64_t R, int64_t C, int64_t slab_rows,
                             int64_t splits, cudaStream_t st) {
@@ -1902,7 +1924,7 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
     void* dz = ws + p.dz_off;
     void* slab_h = ws + p.dh_off;
     void* slab_w = ws + p.dw_off;
-    CUtensorMap mh, mw, mdz, ma, mb;
+    CUtensorMap mh, mw, mdz;
     if (!map_kmajor(&mh, H, M, K, sru::gemm::P_CM)) return SRU_ERR_INVALID;
     sru::loss::LossArgs a{};
     a.targets = reinterpret_cast<const long long*>(targets);
@@ -1917,16 +1939,24 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
     // dH is summed over the pieces in fp32: in place, or in the workspace when it is split
     // along the vocabulary or leaves as bf16
     const bool h_in_slabs = p.dh.splits > 1 || (p.pieces > 1 && dh_t == SRU_BF16);
-    using sru::gemm::kOutBF16;
-    using sru::gemm::kOutF32;
-    using sru::gemm::kOutF32Acc;
+    const bool w_in_slabs = p.dw.splits > 1;
+    // an output of the gradient products: rows x K of type t, in boxes of 32 rows x 128 bytes
+    auto map_out = [&](CUtensorMap* m, void* out, int t, int64_t rows) {
+        const bool bf = t == SRU_BF16;
+        const uint64_t dims[2] = {(uint64_t)K, (uint64_t)rows}, strides[1] = {(uint64_t)K * (bf ? 2 : 4)};
+        const uint32_t box[2] = {bf ? 64u : 32u, 32};
+        return make_map(m, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, out, dims,
+                        strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    CUtensorMap mhm;
+    if (!map_mnmajor(&mhm, H, K, M, K)) return SRU_ERR_INVALID;
     for (int64_t v0 = 0; v0 < V; v0 += p.Vc) {
         const int64_t n = std::min(p.Vc, V - v0);
         const __nv_bfloat16* Wp = static_cast<const __nv_bfloat16*>(W) + (size_t)v0 * K;
         {
             const uint64_t dims[2] = {(uint64_t)n, (uint64_t)M};
             const uint64_t strides[1] = {(uint64_t)p.Vc * 2};
-            const uint32_t box[2] = {(uint32_t)sru::gemm::EpiChunk<kOutBF16>::kCols, 32};
+            const uint32_t box[2] = {64, 32};
             if (!map_kmajor(&mw, Wp, n, K, kGemmBRows) ||
                 !make_map(&mdz, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, dz, dims, strides, box,
                           CU_TENSOR_MAP_SWIZZLE_128B))
@@ -1935,42 +1965,52 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
         a.v0 = v0;
         s = launch_vocab<sru::loss::kGrad>(p.warps, mh, mw, mdz, a, M, n, K, st);
         if (s != SRU_OK) return s;
-        if (dH) {
-            // dH += dz W: A = dz (M x n) K-major, B(c = k, red = v) = W[v][k] MN-major
-            if (!map_kmajor(&ma, dz, M, n, sru::gemm::P_CM, p.Vc) || !map_mnmajor(&mb, Wp, K, n, K))
-                return SRU_ERR_INVALID;
-            if (p.dh.splits > 1) {
-                // no empty part in a shorter last piece either (see split_plan)
-                const int64_t kb = (n + sru::gemm::BK - 1) / sru::gemm::BK;
-                const int64_t per = (kb + p.dh.splits - 1) / p.dh.splits, S = (kb + per - 1) / per;
-                s = v0 == 0 ? launch_slabs<false, true, kOutF32>(ma, mb, slab_h, M, K, n, S, p.dh.slab_rows,
-                                                                 p.dh.splits, scale, st)
-                            : launch_slabs<false, true, kOutF32Acc>(ma, mb, slab_h, M, K, n, S, p.dh.slab_rows,
-                                                                    p.dh.splits, scale, st);
-            } else {
-                void* out = h_in_slabs ? slab_h : dH;
-                if (v0 != 0) s = launch_tc_gemm<false, true, kOutF32Acc, true>(ma, mb, out, M, K, n, st, 1, -1, false, scale);
-                else if (!h_in_slabs && dh_t == SRU_BF16)
-                    s = launch_tc_gemm<false, true, kOutBF16, true>(ma, mb, out, M, K, n, st, 1, -1, false, scale);
-                else s = launch_tc_gemm<false, true, kOutF32, true>(ma, mb, out, M, K, n, st, 1, -1, /*tail_split=*/true, scale);
-            }
-            if (s != SRU_OK) return s;
+        // dH (+)= dz W: A = dz (M x n) K-major, B(c = k, red = v) = W[v][k] MN-major;
+        // this piece's rows of dW = dz^T H: A = dz read as (n x M) MN-major, B(c = k, red = m) = H[m][k]
+        CUtensorMap mzk, mzm, mwm, moh, mow;
+        void* out_w = static_cast<uint8_t*>(dW) + (size_t)v0 * K * (dw_t == SRU_BF16 ? 2 : 4);
+        if (!map_kmajor(&mzk, dz, M, n, sru::gemm::P_CM, p.Vc) || !map_mnmajor(&mzm, dz, n, M, p.Vc) ||
+            !map_mnmajor(&mwm, Wp, K, n, K))
+            return SRU_ERR_INVALID;
+        sru::loss::GradArgs g{};
+        g.K = (int)K;
+        g.scale = scale;
+        const int64_t rows[2] = {M, n}, red[2] = {n, M};
+        const SplitPlan* plan[2] = {&p.dh, &p.dw};
+        const bool on[2] = {dH != nullptr, dW != nullptr}, slabs[2] = {h_in_slabs, w_in_slabs};
+        const int type[2] = {dh_t, dw_t};
+        for (int i = 0; i < 2; ++i) {
+            sru::loss::GradProblem& q = g.p[i];
+            const int64_t kb = (red[i] + sru::gemm::BK - 1) / sru::gemm::BK;
+            const int64_t per = (kb + plan[i]->splits - 1) / plan[i]->splits;
+            q.splits = (int)((kb + per - 1) / per);  // no empty part in a shorter last piece either
+            q.kper = (int)((kb + q.splits - 1) / q.splits);
+            q.kblocks = (int)kb;
+            q.rows = (int)rows[i];
+            q.n_tiles = (int)((K + sru::gemm::P_BN - 1) / sru::gemm::P_BN);
+            const int64_t units = ((rows[i] + sru::gemm::P_BM - 1) / sru::gemm::P_BM) * q.n_tiles * q.splits;
+            if (units >= (int64_t)1 << 30) return SRU_ERR_UNSUPPORTED;
+            q.units = on[i] ? (int)units : 0;
+            q.slab_rows = (int)plan[i]->slab_rows;
+            q.bf16 = !slabs[i] && type[i] == SRU_BF16;
+            q.add = i == 0 && v0 != 0;
         }
-        if (dW) {
-            // this piece's rows of dW = dz^T H: A = dz read as (n x M) MN-major, B(c = k, red = m) = H[m][k]
-            if (!map_mnmajor(&ma, dz, n, M, p.Vc) || !map_mnmajor(&mb, H, K, M, K)) return SRU_ERR_INVALID;
-            void* out = static_cast<uint8_t*>(dW) + (size_t)v0 * K * (dw_t == SRU_BF16 ? 2 : 4);
-            if (p.dw.splits > 1) {
-                s = launch_slabs<true, true, kOutF32>(ma, mb, slab_w, n, K, M, p.dw.splits, p.dw.slab_rows,
-                                                      p.dw.splits, scale, st);
-                if (s == SRU_OK) s = sum_slabs(slab_w, out, dw_t, n, K, p.dw.slab_rows, p.dw.splits, st);
-            } else if (dw_t == SRU_BF16) {
-                s = launch_tc_gemm<true, true, kOutBF16, true>(ma, mb, out, n, K, M, st, 1, -1, false, scale);
-            } else {
-                s = launch_tc_gemm<true, true, kOutF32, true>(ma, mb, out, n, K, M, st, 1, -1, /*tail_split=*/true, scale);
-            }
-            if (s != SRU_OK) return s;
-        }
+        if (!(dH ? map_out(&moh, h_in_slabs ? slab_h : dH, h_in_slabs ? SRU_F32 : dh_t,
+                           p.dh.splits > 1 ? p.dh.slab_rows * p.dh.splits : M)
+                 : (moh = mzk, true)) ||
+            !(dW ? map_out(&mow, w_in_slabs ? slab_w : out_w, w_in_slabs ? SRU_F32 : dw_t,
+                           w_in_slabs ? p.dw.slab_rows * p.dw.splits : n)
+                 : (mow = mzk, true)))
+            return SRU_ERR_INVALID;
+        g.extra = (int)grad_extra(grad_unit_us(g.p[0].kper), grad_unit_us(g.p[1].kper));
+        auto kern = sru::loss::vocab_grad_kernel;
+        SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kern), sru::gemm::P_SMEM_BYTES));
+        const int64_t pairs = std::min<int64_t>((int64_t)g.p[0].units + g.p[1].units, sm_count() / 2);
+        s = launch_overlapped(kern, dim3((unsigned)(2 * pairs)), sru::gemm::THREADS, sru::gemm::P_SMEM_BYTES, st, mzk, mwm,
+                              mzm, mhm, moh, mow, g);
+        if (s == SRU_OK && dW && w_in_slabs)
+            s = sum_slabs(slab_w, out_w, dw_t, n, K, p.dw.slab_rows, g.p[1].splits, st);
+        if (s != SRU_OK) return s;
     }
     if (dH && h_in_slabs) return sum_slabs(slab_h, dH, dh_t, M, K, p.dh.slab_rows, p.dh.splits, st);
     return SRU_OK;

@@ -236,13 +236,11 @@ __device__ __forceinline__ bool pair_next(int i, int p, int P, int units, int m_
     return true;
 }
 
-// CHAIN: a product in a chain of overlapped launches (see pdl_wait), whose output is
-// multiplied by *out_scale (fp32, before the rounding to the output type).
-template <bool A_MN, bool B_MN, int OUT, int BPA = 0, int BPB = 0, int CAUSAL = 0, int BPO = 0, bool CHAIN = false>
+template <bool A_MN, bool B_MN, int OUT, int BPA = 0, int BPB = 0, int CAUSAL = 0, int BPO = 0>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     tc_gemm_pair_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                         const __grid_constant__ CUtensorMap map_out, int M, int N, int K, int splits, int batches,
-                        int tail_s, int slab_rows, const float* __restrict__ out_scale) {
+                        int tail_s, int slab_rows) {
     static_assert(((BPA | BPB) == 0) == (BPO == 0), "batched launches store through a 3-D output map");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -294,10 +292,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t tmem_base = *tmem_slot;
     const uint32_t leader_full0 = mapa_shared(smem_u32(&full[0]), 0);
     const uint32_t leader_tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
-    if (CHAIN) {
-        pdl_launch();
-        pdl_wait();
-    }
 
     if (warp == 0) {
         if (lane == 0) {
@@ -404,7 +398,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     } else {
         // ---------------------------------------------------------- epilogue (both CTAs)
         const int quarter = warp & 3;
-        const float scale = CHAIN ? *out_scale : 1.f;
         int it = 0;
         uint32_t nstaged = 0;  // chunks this warp has handed to TMA stores
         PairUnit w;
@@ -435,10 +428,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 uint32_t(&nxt)[NC] = (g & 1) ? r0 : r1;
                 tc_wait_ld();  // chunk g (and nothing else) is in flight
                 if (g + 1 < ng) tmem_ld_cols<NC>(tacc + (g + 1) * NC, nxt);
-                if (CHAIN) {
-#pragma unroll
-                    for (int e = 0; e < NC; ++e) cur[e] = __float_as_uint(__uint_as_float(cur[e]) * scale);
-                }
                 const int col0 = n0 + g * NC;
                 // buffer (nstaged & 1) was last read by the store issued two chunks ago
                 const uint32_t buf = smem_u32(epi) + (uint32_t)(quarter * 2 + (nstaged & 1)) * P_EPI_BUF;

@@ -23,6 +23,8 @@
 // more than the product for K up to about 2000.
 #pragma once
 
+#include <type_traits>
+
 #include "sru_gemm.cuh"
 
 namespace sru {
@@ -296,6 +298,265 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + W * 32, 1)
             if (EPI == kStats && live) a.partial[(size_t)(kParts * tn + part) * M + row] = make_float2(top, sum);
         }
         if (EPI == kGrad && lane == 0) bulk_wait_group<0>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem_base, P_TMEM_COLS);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Both gradient products of a piece in one launch: dH (+)= dz W (problem 0) and
+// dW = dz^T H (problem 1), the pair GEMM's pipeline over one list of work units, so
+// that neither product's last, partial round of CTA pairs is waited for, nor a launch
+// between them.  A unit is an output tile and one k part of it.  (Tiles of 128
+// columns for a K that fills its last 256 badly were slower: 12% at K520.)
+struct GradProblem {
+    int units, n_tiles, splits, kblocks, kper, slab_rows, rows;  // rows: of the output
+    int bf16, add;  // output type; add onto the output (fp32)
+};
+struct GradArgs {
+    GradProblem p[2];
+    int K, extra;        // extra: units of problem 1 that a pair without a last one of problem 0 takes first
+    const float* scale;  // the outputs are multiplied by it
+};
+struct GradUnit {
+    int prob, tm, tn, split, kb_lo, kb_hi;
+};
+// The i-th unit of pair q (of P): its units of problem 0 (q, q + P, ..); then, while
+// the first r = units0 % P pairs are busy with one more, the others take `extra` units
+// of problem 1 each; then the rest of problem 1 round-robin, the last pairs first.
+__device__ __forceinline__ bool grad_unit(const GradArgs& a, int i, int q, int P, GradUnit& w) {
+    const int u0 = a.p[0].units, own = (u0 - q + P - 1) / P, r = u0 % P;
+    int u;
+    if (i < own) {
+        w.prob = 0;
+        u = q + i * P;
+    } else {
+        w.prob = 1;
+        i -= own;
+        const int x = r > 0 && q >= r ? a.extra : 0;
+        if (i < x) u = (q - r) + i * (P - r);
+        else u = (r > 0 ? a.extra * (P - r) : 0) + (P - 1 - q) + (i - x) * P;
+        if (u >= a.p[1].units) return false;
+    }
+    const GradProblem& p = a.p[w.prob];
+    const int tile = u / p.splits;
+    w.split = u - tile * p.splits;
+    w.tm = tile / p.n_tiles;
+    w.tn = tile - w.tm * p.n_tiles;
+    w.kb_lo = w.split * p.kper;
+    w.kb_hi = min(p.kblocks, w.kb_lo + p.kper);
+    return true;
+}
+
+// One output tile's rows of this warp: TMEM -> scaled, rounded -> staging -> TMA.
+template <int OUT>
+__device__ __forceinline__ void grad_epilogue(uint32_t tacc, int ncol, float scale, uint8_t* bufs, uint32_t& nstaged,
+                                              const CUtensorMap* map, bool add, int n0, int row, int lane) {
+    constexpr int NC = EpiChunk<OUT>::kCols;
+    const int ng = (ncol + NC - 1) / NC;
+    uint32_t r0[NC], r1[NC];
+    tmem_ld_cols<NC>(tacc, r0);
+#pragma unroll
+    for (int g = 0; g < P_BN / NC; ++g) {
+        if (g >= ng) break;  // uniform across the warp
+        uint32_t(&cur)[NC] = (g & 1) ? r1 : r0;
+        uint32_t(&nxt)[NC] = (g & 1) ? r0 : r1;
+        tc_wait_ld();
+        if (g + 1 < ng) tmem_ld_cols<NC>(tacc + (g + 1) * NC, nxt);
+#pragma unroll
+        for (int e = 0; e < NC; ++e) cur[e] = __float_as_uint(__uint_as_float(cur[e]) * scale);
+        uint8_t* buf = bufs + (nstaged & 1) * P_EPI_BUF;
+        if (lane == 0) bulk_wait_group_read<1>();  // its last store has read it
+        __syncwarp();
+        epilogue_stage_row<OUT>(smem_u32(buf), lane, cur);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            if (add) tma_reduce_add_2d(map, buf, n0 + g * NC, row);
+            else tma_store_2d(map, buf, n0 + g * NC, row);
+            bulk_commit_group();
+        }
+        ++nstaged;
+    }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    vocab_grad_kernel(const __grid_constant__ CUtensorMap map_dz_k, const __grid_constant__ CUtensorMap map_w,
+                      const __grid_constant__ CUtensorMap map_dz_m, const __grid_constant__ CUtensorMap map_h,
+                      const __grid_constant__ CUtensorMap map_dh, const __grid_constant__ CUtensorMap map_dw,
+                      const __grid_constant__ GradArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* epi = smem + P_STAGES * P_STAGE_BYTES;
+    uint64_t* full = reinterpret_cast<uint64_t*>(epi + P_EPI_BYTES);
+    uint64_t* empty = full + P_STAGES;
+    uint64_t* tfull = empty + P_STAGES;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* drain = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile uint32_t* consumed = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair_id = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < P_STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 8);  // 4 epilogue warps of each CTA
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        *consumed = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&map_dz_k);
+        tma_prefetch_desc(&map_w);
+        tma_prefetch_desc(&map_dz_m);
+        tma_prefetch_desc(&map_h);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, P_TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before_sync();
+    cluster_sync_all();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t leader_full0 = mapa_shared(smem_u32(&full[0]), 0);
+    const uint32_t leader_tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    pdl_launch();
+    pdl_wait();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------------ producer (both CTAs)
+            uint32_t issued = 0, phase = 0;
+            int stage = 0;
+            GradUnit w;
+            for (int i = 0; !*abort_flag && grad_unit(a, i, pair_id, n_pairs, w); ++i) {
+                const int m0 = w.tm * P_BM + (int)rank * P_CM, n0 = w.tn * P_BN + (int)rank * P_CN;
+                // (a loop per problem: with the maps chosen inside, the loads were late and a long
+                // product 8% slower)
+                auto kblocks = [&](auto second) {
+                    constexpr bool P1 = decltype(second)::value;
+                    for (int kb = w.kb_lo; kb < w.kb_hi; ++kb) {
+                        if (!mbar_wait(&empty[stage], phase ^ 1u, kErrTimeoutMma) || *abort_flag) {
+                            *abort_flag = 1;
+                            break;
+                        }
+                        uint8_t* a_dst = smem + stage * P_STAGE_BYTES;
+                        uint8_t* b_dst = a_dst + P_A_BYTES;
+                        const uint32_t bar = leader_full0 + (uint32_t)stage * 8u;
+                        if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * P_STAGE_BYTES);
+                        if (P1) {
+                            tma_load_2d_pair(a_dst, &map_dz_m, bar, m0, kb * BK);
+                            tma_load_2d_pair(a_dst + MN_BOX_BYTES, &map_dz_m, bar, m0 + 64, kb * BK);
+                            tma_load_2d_pair(b_dst, &map_h, bar, n0, kb * BK);
+                            tma_load_2d_pair(b_dst + MN_BOX_BYTES, &map_h, bar, n0 + 64, kb * BK);
+                        } else {
+                            tma_load_2d_pair(a_dst, &map_dz_k, bar, kb * BK, m0);
+                            tma_load_2d_pair(b_dst, &map_w, bar, n0, kb * BK);
+                            tma_load_2d_pair(b_dst + MN_BOX_BYTES, &map_w, bar, n0 + 64, kb * BK);
+                        }
+                        ++issued;
+                        if (++stage == P_STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                };
+                if (w.prob == 0) kblocks(std::false_type{});
+                else kblocks(std::true_type{});
+            }
+            if (*abort_flag && rank == 0) {
+                for (uint32_t q = *consumed; q < issued; ++q)
+                    mbar_wait(&full[q % P_STAGES], (q / P_STAGES) & 1u, kErrTimeoutLoad);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ------------------------------------------------------ MMA issuer (leader)
+            int stage = 0;
+            uint32_t phase = 0, nconsumed = 0;
+            GradUnit w;
+            for (int i = 0; !*abort_flag && grad_unit(a, i, pair_id, n_pairs, w); ++i) {
+                const int acc = i & 1;
+                if (!mbar_wait(&tempty[acc], ((i >> 1) & 1) ^ 1u, kErrTimeoutEpilogue)) {
+                    *abort_flag = 1;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + acc * P_BN;
+                auto kblocks = [&](auto a_mn) {
+                    constexpr bool A_MN = decltype(a_mn)::value;
+                    constexpr uint32_t idesc = idesc_bf16_pair(A_MN, true);
+                    for (int kb = w.kb_lo; kb < w.kb_hi; ++kb) {
+                        if (!mbar_wait(&full[stage], phase, kErrTimeoutLoad)) return false;
+                        tc_fence_after_sync();
+                        const uint32_t a_addr = smem_u32(smem + stage * P_STAGE_BYTES), b_addr = a_addr + P_A_BYTES;
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            tc_mma_bf16_pair(d_tmem,
+                                             A_MN ? smem_desc_sw128(a_addr + kk * 2048, MN_BOX_BYTES, 1024)
+                                                  : smem_desc_sw128(a_addr + kk * 32, 16, 1024),
+                                             smem_desc_sw128(b_addr + kk * 2048, MN_BOX_BYTES, 1024), idesc,
+                                             (kb != w.kb_lo || kk != 0) ? 1u : 0u);
+                        tc_commit_pair_mc(&empty[stage], 0x3);
+                        *consumed = ++nconsumed;
+                        if (++stage == P_STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    return true;
+                };
+                const bool ok = w.prob == 0 ? kblocks(std::false_type{}) : kblocks(std::true_type{});
+                if (!ok) {
+                    *abort_flag = 1;
+                    break;
+                }
+                tc_commit_pair_mc(&tfull[acc], 0x3);
+            }
+            tc_commit_pair_mc(drain, 0x1);
+            mbar_wait(drain, 0, kErrTimeoutMma);
+        }
+    } else {
+        // ---------------------------------------------------------- epilogue (both CTAs)
+        const int quarter = warp & 3;
+        const float scale = *a.scale;
+        uint8_t* bufs = epi + (size_t)quarter * 2 * P_EPI_BUF;
+        uint32_t nstaged = 0;
+        GradUnit w;
+        for (int i = 0; grad_unit(a, i, pair_id, n_pairs, w); ++i) {
+            const int acc = i & 1;
+            const bool ok = mbar_wait(&tfull[acc], (i >> 1) & 1, kErrTimeoutMma);
+            if (!__all_sync(0xffffffffu, ok) || *abort_flag) {
+                *abort_flag = 1;
+                break;
+            }
+            tc_fence_after_sync();
+            const GradProblem& p = a.p[w.prob];
+            const int n0 = w.tn * P_BN, ncol = min(P_BN, a.K - n0);
+            const int row = w.tm * P_BM + (int)rank * P_CM + quarter * 32 + w.split * p.slab_rows;
+            const uint32_t tacc = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * P_BN;
+            const CUtensorMap* map = w.prob == 0 ? &map_dh : &map_dw;
+            if (p.bf16) grad_epilogue<kOutBF16>(tacc, ncol, scale, bufs, nstaged, map, false, n0, row, lane);
+            else grad_epilogue<kOutF32>(tacc, ncol, scale, bufs, nstaged, map, p.add, n0, row, lane);
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(leader_tempty0 + (uint32_t)acc * 8u);
+        }
+        if (lane == 0) bulk_wait_group<0>();
     }
     tc_fence_before_sync();
     __syncthreads();
