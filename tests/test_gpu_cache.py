@@ -321,6 +321,56 @@ def test_the_same_bits_every_run_and_alone_or_in_a_batch_shape(sru):
         assert torch.equal(_decode(sru, inp, torch.float32), first)
 
 
+def test_one_workspace_for_calls_of_any_shape_and_two_graphs(sru):
+    """A workspace with anything in it, used by calls of other shapes in turn, and by two
+    captured graphs that are replayed in turn."""
+    shapes = [([20000], 8, 1, 128, 16), ([3000, 0, 700], 2, 1, 512, 32), ([40] * 50, 4, 4, 64, 16),
+              ([9000, 8000], 1, 1, 1024, 64), ([5000] * 3, 16, 2, 96, 24)]
+    inputs = [_decode_inputs(len(l), hq, hkv, d, l, ps, seed=i) for i, (l, hq, hkv, d, ps) in enumerate(shapes)]
+    need = max(sru.sru_attention_decode_workspace_bytes(len(l), hq, hkv, d) for l, hq, hkv, d, _ in shapes)
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
+    outs = [torch.empty(i[0].shape, device="cuda") for i in inputs]
+
+    def call(k):
+        q, kc, vc, table, lengths, K, V = inputs[k]
+        sru.sru_attention_decode(q, kc, vc, table, lengths, outs[k], workspace=ws)
+
+    for k in (0, 1, 2, 3, 4, 3, 1, 0):
+        outs[k].fill_(float("nan"))
+        call(k)
+        assert sru.sru_sync_status() == 0
+        _check_decode(outs[k], None, inputs[k][0], inputs[k][5], inputs[k][6], inputs[k][0].shape[2] ** -0.5, 0)
+    graphs = []
+    for k in (0, 3):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(k)
+        graphs.append((k, g))
+    for _ in range(3):
+        for k, g in graphs:
+            outs[k].fill_(float("nan"))
+            g.replay()
+    assert sru.sru_sync_status() == 0
+    for k in (0, 3):
+        _check_decode(outs[k], None, inputs[k][0], inputs[k][5], inputs[k][6], inputs[k][0].shape[2] ** -0.5, 0)
+
+
+def test_calls_one_after_another_without_a_wait(sru):
+    """Forty calls in a row on one stream, each reading what the one before it wrote."""
+    q, kc, vc, table, lengths, K, V = _decode_inputs(4, 2, 1, 128, [700, 300, 5, 64], 16, seed=8)
+    x, y = q.clone(), torch.empty_like(q)
+    want = q.clone()
+    for _ in range(20):
+        sru.sru_attention_decode(x, kc, vc, table, lengths, y)
+        sru.sru_attention_decode(y, kc, vc, table, lengths, x)
+    for _ in range(40):
+        got = torch.empty_like(q)
+        sru.sru_attention_decode(want, kc, vc, table, lengths, got)
+        assert sru.sru_sync_status() == 0
+        want = got
+    assert torch.equal(x, want)
+
+
 def _serve(sru, on_stream):
     """A few serving steps as a program runs them: extend, append, attend, with
     requests that come, grow and leave; then the same steps replayed from a graph."""

@@ -132,6 +132,49 @@ def test_sharp_and_flat_rows(sru):
     _check(sru, H, W, t, w, torch.float32)
 
 
+@pytest.mark.parametrize("M,V,K", [
+    (2304, 3000, 256),   # whole rounds of dH tiles and a partial one, dW interleaved
+    (18944, 500, 256),   # 74 dH tiles: one whole round on 148 SMs
+    (700, 19000, 1024),
+])
+def test_the_gradients_share_a_launch(sru, M, V, K):
+    _check(sru, *_inputs(M, V, K, seed=2), torch.bfloat16)
+
+
+def test_weights_of_any_size(sru):
+    """dz is held over the largest weight: weights over 30 powers of ten, zeros among
+    them, and NaN and infinity on rows that do not count."""
+    H, W, t, w = _inputs(400, 1200, 64, seed=3)
+    w = torch.logspace(-25, 5, 400, device="cuda")[torch.randperm(400, device="cuda")]
+    w[::7] = 0.0
+    want = w.clone()
+    w[t < 0] = float("nan")
+    w[(t < 0).nonzero()[0]] = float("inf")
+    loss, lse, dH, dW = _run(sru, H, W, t, w, torch.float32)
+    r = _reference(H, W, t, want)
+    # (a weight far below the largest is held over it: smaller than 2^-126 of it, it may vanish)
+    tiny = float(want.max()) * 2.0 ** -126 * W.double().abs().sum(0).max()
+    _within("dH", dH, r["dH"], r["bH"] + 2.0 ** -24 * r["dH"].abs() + tiny)
+    _within("dW", dW, r["dW"], r["bW"] + 2.0 ** -24 * r["dW"].abs() + tiny)
+    assert (dH[want == 0] == 0).all()
+    w = torch.zeros_like(w)
+    _, _, dH, dW = _run(sru, H, W, t, w, torch.float32)
+    assert (dH == 0).all() and (dW == 0).all()
+
+
+def test_equal_weights_do_not_share_a_rounding_error(sru):
+    """1 / 1001 is 2.7e-3 off in bf16.  The gradients' norm is not off by that: every
+    row's p - 1 is rounded on its own, so the sum over 64 x 1001 of them is within a
+    fifth of half a step."""
+    H, W, t, _ = _inputs(1001, 5000, 64, ignored=0.0, seed=4)
+    w = torch.full((1001,), 1.0 / 1001, device="cuda")
+    _, _, dH, dW = _run(sru, H, W, t, w, torch.float32)
+    r = _reference(H, W, t, w)
+    for got, ref in ((dH, r["dH"]), (dW, r["dW"])):
+        along = float((got.double() * ref).sum() / (ref * ref).sum())
+        assert abs(along - 1) < 0.2 * 2.0 ** -8
+
+
 def test_no_row_counts(sru):
     H, W, t, w = _inputs(70, 500, 64)
     t.fill_(-1)
