@@ -211,9 +211,14 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
         return;
     }
     const int total = (int)total64;
-    // steps per team; at most about 64 CTAs share an item, whose pieces one of them joins
+    // Steps per team.  Few items leave few steps to each, but an item's pieces have to be joined
+    // by one CTA: about 0.75 us per eight CTAs that share it and task (head and slice) of a
+    // warp, against 2 us for a step more, whose sum is least at this square root.  (One step:
+    // B2 H16/1 D1024 len <= 2311 takes 75 us, B3 H4/1 D768 len <= 5000 51 us.)
     const int n_teams = gridDim.x * teams;
-    const int per = max(max((total + n_teams - 1) / n_teams, (longest + 64 * teams - 1) / (64 * teams)), 1);
+    const float tasks_per_warp = (float)(min(8, a.group) * tw) / n_warps;
+    const int least = (int)sqrtf(0.045f * fmaxf(tasks_per_warp, 1.f) * longest / teams);
+    const int per = max(max((total + n_teams - 1) / n_teams, least), 1);
     s_before[tid] = (int)before;
     __syncthreads();
 
