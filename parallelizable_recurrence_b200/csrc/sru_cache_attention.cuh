@@ -30,6 +30,8 @@
 // scores make it; the second product is free next to the loads.
 #pragma once
 
+#include <type_traits>
+
 #include "sru_ptx.cuh"
 
 namespace sru {
@@ -583,8 +585,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
 
     // ---- joining.  One head and 128 features of n pieces per warp, a lane four features:
     // unnormalised sum, m and l; load_o(i) gives piece i's four features, load_ml(i, j) its m and l.
-    auto join = [&](int n, auto load_o, auto load_ml, float4& acc, float& top, float& l) {
-        constexpr int kAhead = 8;
+    auto join = [&](auto ahead, int n, auto load_o, auto load_ml, float4& acc, float& top, float& l) {
+        constexpr int kAhead = decltype(ahead)::value;  // pieces whose loads are in flight
         top = -INFINITY;
         l = 0.f;
         acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -669,7 +671,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             auto load_ml = [&](int i, int j) { return s_ml[from + i][i == 0 ? kind : 0][j + head]; };
             float4 acc;
             float top, l;
-            join(n, load_o, load_ml, acc, top, l);
+            join(std::integral_constant<int, kMaxWarps>{}, n, load_o, load_ml, acc, top, l);
             if (whole) {
                 store(it, head, slice, acc, top, l);
             } else {
@@ -731,7 +733,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             float4 acc;
             float top, l;
             // (written by other SMs while this kernel runs: past L1)
-            join(n,
+            join(std::integral_constant<int, 16>{}, n,
                  [&](int i) {
                      return __ldcg(reinterpret_cast<const float4*>(a.part + index(i) * pf +
                                                                    (size_t)slice * kSliceFloats + head * kSlice) + lane);
