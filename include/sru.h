@@ -382,9 +382,10 @@ sru_status sru_softmax_loss(const void* H, const void* W, const int64_t* targets
  * each of type F32 or BF16 (dh_t, dw_t), written; either may be NULL (not
  * computed).  H, W, targets as given to the forward, lse as it wrote it.
  * The logits are recomputed one piece of the vocabulary at a time; dz of a
- * piece is rounded to bf16 (it is a tensor-core operand), the sums over the
- * vocabulary and over the rows are fp32 and taken in a fixed order (the same
- * bits every run).  M = 0 writes dW = 0.
+ * piece, over the largest |dloss| of a counted row, is rounded to bf16 (it is a
+ * tensor-core operand; a weight below 2^-126 of the largest may vanish), the
+ * sums over the vocabulary and over the rows are fp32 and taken in a fixed order
+ * (the same bits every run).  M = 0 writes dW = 0.
  * workspace: >= sru_softmax_loss_workspace_bytes(M, V, K, 1) bytes (which also
  * serves the forward).  Limits as for the forward.
  */
@@ -401,7 +402,7 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
  *     table[b][t / page_size]; entries behind its last page are not read
  *   slot of a token: table[b][t / page_size] * page_size + t % page_size
  *   free_pages (pages) int32: a stack of the pages that no request holds,
- *     *free_count of them
+ *     *free_count of them; a page is held by one request
  *
  * sru_cache_extend: the bookkeeping of one serving step, from device-side
  * lengths, without a host round trip.  Request b holds lengths[b] tokens and

@@ -1986,7 +1986,6 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
             q.splits = (int)((kb + per - 1) / per);  // no empty part in a shorter last piece either
             q.kper = (int)((kb + q.splits - 1) / q.splits);
             q.kblocks = (int)kb;
-            q.rows = (int)rows[i];
             q.n_tiles = (int)((K + sru::gemm::P_BN - 1) / sru::gemm::P_BN);
             const int64_t units = ((rows[i] + sru::gemm::P_BM - 1) / sru::gemm::P_BM) * q.n_tiles * q.splits;
             if (units >= (int64_t)1 << 30) return SRU_ERR_UNSUPPORTED;
@@ -2025,9 +2024,10 @@ static sru_status check_cache_sizes(int64_t pages, int64_t ps) {
 }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Rows from which a second kernel writes the slots (one CTA writes about 1000 rows a
-// microsecond next to its sums; the second launch costs about 3).
-constexpr int64_t kExtendRowsKernel = 4096;
+// Rows from which a second kernel writes the slots.  Measured with / without it, prompts among
+// the requests: 14.2 / 13.8 us at 1500 rows (B8), 14.3 / 15.4 at 3285 (B16), 14.5 / 38.9 at 5285
+// (B30).
+constexpr int64_t kExtendRowsKernel = 2048;
 
 sru_status sru_cache_extend(const int32_t* lengths, const int32_t* new_tokens, int32_t* table, int32_t* free_pages,
                             const int32_t* free_count, int64_t B, int64_t max_pages, int64_t pages, int64_t page_size,
@@ -2095,14 +2095,14 @@ struct DecodePlan {
 };
 static DecodePlan decode_plan(int64_t Hq, int64_t Hkv, int64_t D) {
     DecodePlan p{};
-    // 64 features per warp for D = 64, else 128 (D192, B64 H2 len <= 4000: 58 us as 128 + 64, 71 us
-    // as 3 x 64)
+    // 64 features per warp for D = 64, else 128 (B64 H2 len <= 4000 D192: 58 us as 128 + 64, 71 us as
+    // 3 x 64)
     p.width = D == 64 ? 64 : sru::cache::kSlice;
     p.tw = (int)((D + p.width - 1) / p.width);
     p.teams = sru::cache::kMaxWarps / p.tw;
     p.blocks = (int)((Hq / Hkv + 7) / 8);
-    // a ring of 24 KB per warp, 32 KB for up to six warps
-    p.units = (p.tw * p.teams <= 6 ? 4 : 3) * (D <= 64 || p.width == 64 ? 2 : 1);
+    // a ring of 24 KB per warp (32 KB, which six warps leave room for, was not faster)
+    p.units = 3 * (D <= 64 ? 2 : 1);
     // two pieces per CTA, a slice per warp for pieces that end early
     const size_t ctas = (size_t)sm_count();
     p.flags_off = round256((ctas * 2 * sru::cache::piece_floats(p.tw) +
@@ -2172,7 +2172,7 @@ sru_status sru_attention_decode(const void* q, const void* k_cache, const void* 
     // the rings, and room for the pieces that end early where it is left (the static part is
     // the scores' exchange, which a team of one warp does not have)
     a.units = p.units;
-    const size_t unit = (D <= 64 || p.width == 64 ? 1 : 2) * sru::cache::kHalfBytes;
+    const size_t unit = (D <= 64 ? 1 : 2) * sru::cache::kHalfBytes;
     const size_t rings = (size_t)p.tw * p.teams * p.units * unit + 1024;
     const size_t early = (size_t)p.tw * p.teams * std::min<int64_t>(8, a.group) * sru::cache::kSlice * sizeof(float);
     const size_t most = (size_t)(D == 128 ? 225 : D == 64 ? 224 : 207) * 1024;
@@ -2180,8 +2180,10 @@ sru_status sru_attention_decode(const void* q, const void* k_cache, const void* 
     const size_t smem = rings + (fits ? early : 0);
     a.early_floats = fits ? (int)(early / sizeof(float)) / (p.tw * p.teams) : 0;
     using sru::cache::cache_attention_kernel;
-    auto kern = cache_attention_kernel<0, 0>;  // any D
-    switch (D) {                               // the forms without loops over the width
+    // any D, or a form without loops over the width (B64 H2 len <= 4000: D64 33 -> 27.5 us, D384
+    // 100 -> 82, D768 193 -> 160)
+    auto kern = cache_attention_kernel<0, 0>;
+    switch (D) {
         case 64: kern = cache_attention_kernel<1, 64>; break;
         case 128: kern = cache_attention_kernel<1, 128>; break;
         case 256: kern = cache_attention_kernel<2, 128>; break;

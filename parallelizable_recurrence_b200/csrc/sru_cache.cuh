@@ -28,6 +28,8 @@ namespace cache {
 // request's own thread or warp can write.  A step with room for many rows gets a
 // second kernel over the rows for the requests of more than kExtDirect tokens; it
 // learns from such a request's first slot, written here, whether it was refused.
+// (A cluster of 8 CTAs that all made the sums took 47 us where this takes 16: B1024 with
+// 600 thousand rows; a step of B48 takes 9, most of it the call itself.)
 constexpr int kExtThreads = 1024;
 constexpr int kExtDirect = 4;  // tokens that a request's own thread writes
 
@@ -253,7 +255,8 @@ __global__ void __launch_bounds__(256) cache_slots_kernel(ExtendArgs a) {
 // -------------------------------------------------------------------------- append
 // Row r of K and V (T rows of Hkv * D elements, k_ld / v_ld apart) to slot
 // slots[r] of the caches, rounded to bf16; a negative slot writes nothing.  Pure
-// copy, bound by memory: 16-byte items, four in flight per thread.
+// copy, bound by memory: 16-byte items, four in flight per thread (16384 rows of K and
+// V, d' 512: 67 MB in 12.1 us, 5.6 TB/s; one item per thread: 18.6 us).
 template <typename SrcT>
 __device__ __forceinline__ uint4 load8_bf16(const SrcT* p) {
     if (sizeof(SrcT) == 2) return __ldg(reinterpret_cast<const uint4*>(p));

@@ -28,6 +28,11 @@
 // exchange nor the products' latency is waited for.  p enters its product as two
 // bf16 parts (value and remainder, 16 bits together), so o is as exact as fp32
 // scores make it; the second product is free next to the loads.
+//
+// Measured: B96 len <= 8192 D1024 277-301 us (6.0-6.5 TB/s, of 6.56 copied), B24 H32/8
+// D128 len <= 6007 67-72 us, B64 D512 window 2560 57 us (4.7-4.9 TB/s): reading at the
+// memory's rate, plus about 12 us that a call of any size takes (5 to the first loads, 2 to
+// the rate, 4-5 to join) and the spread of the warps' ends.
 #pragma once
 
 #include <type_traits>
@@ -41,7 +46,6 @@ constexpr int kStep = 32;     // keys per step
 constexpr int kSlice = 128;   // most features per warp
 constexpr int kMaxWarps = 8;  // per CTA
 constexpr uint32_t kHalfBytes = kStep * 128;        // 64 features of a step's rows
-constexpr uint32_t kRingBytes = 8 * kHalfBytes;     // per warp, at most
 constexpr int kMasks = 8;     // steps whose keys' mask is held
 
 struct DecodeArgs {
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     constexpr int kWidth = W > 0 ? W : kSlice;             // features per warp
-    constexpr int kUnits = W == 64 || W == 0 ? 8 : 4;      // most units of a ring
+    constexpr int kUnits = W == 64 || W == 0 ? 6 : 3;      // most units of a ring
     constexpr bool kExch = TW != 1;
     __shared__ float4 exch[kExch ? 2 : 1][kExch ? kMaxWarps : 1][kExch ? 2 : 1][kExch ? 32 : 1];
     __shared__ uint64_t s_full[kMaxWarps][kUnits];
@@ -255,316 +259,316 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                                        : a.part + (size_t)gridDim.x * 2 * piece_floats(tw) +
                                              (size_t)blockIdx.x * kMaxWarps * kSliceFloats;
     if (n_steps > 0) {
-    const int f0 = w_in * kWidth;                                   // first feature of this warp
-    const int width = W > 0 ? W : min(kSlice, a.D - f0);            // its features, a multiple of 8
-    const int halves = W > 0 ? W / 64 : (a.D > 64 ? 2 : 1);         // boxes of 64 features per row group
-    const uint32_t unit_bytes = halves * kHalfBytes;
+        const int f0 = w_in * kWidth;                                   // first feature of this warp
+        const int width = W > 0 ? W : min(kSlice, a.D - f0);            // its features, a multiple of 8
+        const int halves = W > 0 ? W / 64 : (a.D > 64 ? 2 : 1);         // boxes of 64 features per row group
+        const uint32_t unit_bytes = halves * kHalfBytes;
 
-    // ---- loads.  Lane l has the box of row group l; units come in the order of use: K of step
-    // 0, then K of step j + 1 and V of step j, at last V of the last step.
-    const int R = a.box_rows, groups = kStep / R;
-    const int boxes = a.merged ? 1 : (width > 64 ? 2 : 1);
-    const uint32_t box_bytes = R * 128 * (a.merged ? halves : 1);
-    Cursor ld = cur;
-    int next_page = 0, next_in = -1;  // table entry of this lane's box of step `ld`; < 0: no key of it is wanted
-    auto fetch_page = [&]() {         // (read one step before its load, so that its latency is not waited for)
-        const int pos = ld.s * kStep + lane * R;
-        next_in = -1;
-        if (lane < groups && pos + R > ld.sp.lo && pos < ld.sp.hi) {
-            const int p = pos / a.ps;
-            next_page = __ldg(a.table + (size_t)ld.b * a.maxp + p);
-            next_in = pos - p * a.ps;
-        }
-    };
-    int k_row = 0, k_in = -1, v_row = 0, v_in = -1;  // this lane's box of the step whose K (V) is loaded
-    uint32_t k_bytes = 0, v_bytes = 0;
-    int k_next = 0, v_next = 0, load_stage = 0;      // steps whose K and V come next
-    bool dead = false;                               // a wait ran out: no further loads or waits
-    auto load_next = [&]() {
-        if (v_next >= n_steps || dead) return;
-        const bool is_k = k_next < n_steps && k_next <= v_next + 1;
-        if (is_k || v_next + 1 == k_next) {  // (the last V has no K after it)
-            v_row = k_row;
-            v_in = k_in;
-            v_bytes = k_bytes;
-        }
-        if (is_k) {
-            k_in = next_in;
-            if (k_in >= 0 && (unsigned)next_page >= (unsigned)a.pages) {
-                record_error(kErrBadIndex);  // its keys are left out
-                k_in = -1;
+        // ---- loads.  Lane l has the box of row group l; units come in the order of use: K of step
+        // 0, then K of step j + 1 and V of step j, at last V of the last step.
+        const int R = a.box_rows, groups = kStep / R;
+        const int boxes = a.merged ? 1 : (width > 64 ? 2 : 1);
+        const uint32_t box_bytes = R * 128 * (a.merged ? halves : 1);
+        Cursor ld = cur;
+        int next_page = 0, next_in = -1;  // table entry of this lane's box of step `ld`; < 0: no key of it is wanted
+        auto fetch_page = [&]() {         // (read one step before its load, so that its latency is not waited for)
+            const int pos = ld.s * kStep + lane * R;
+            next_in = -1;
+            if (lane < groups && pos + R > ld.sp.lo && pos < ld.sp.hi) {
+                const int p = pos / a.ps;
+                next_page = __ldg(a.table + (size_t)ld.b * a.maxp + p);
+                next_in = pos - p * a.ps;
             }
-            k_row = (int)((unsigned)next_page * a.Hkv + ld.hh / a.blocks);
-            const unsigned there = __ballot_sync(0xffffffffu, k_in >= 0);
-            k_bytes = __popc(there) * boxes * box_bytes;
-            const int pos = ld.s * kStep + lane;
-            const unsigned mask =
-                __ballot_sync(0xffffffffu, pos >= ld.sp.lo && pos < ld.sp.hi && ((there >> (lane / R)) & 1));
-            if (lane == 0) s_mask[warp][k_next & (kMasks - 1)] = mask;
-            if (++k_next < n_steps) {
-                ld.next(a);
-                fetch_page();
+        };
+        int k_row = 0, k_in = -1, v_row = 0, v_in = -1;  // this lane's box of the step whose K (V) is loaded
+        uint32_t k_bytes = 0, v_bytes = 0;
+        int k_next = 0, v_next = 0, load_stage = 0;      // steps whose K and V come next
+        bool dead = false;                               // a wait ran out: no further loads or waits
+        auto load_next = [&]() {
+            if (v_next >= n_steps || dead) return;
+            const bool is_k = k_next < n_steps && k_next <= v_next + 1;
+            if (is_k || v_next + 1 == k_next) {  // (the last V has no K after it)
+                v_row = k_row;
+                v_in = k_in;
+                v_bytes = k_bytes;
             }
-        } else {
-            ++v_next;
-        }
-        uint64_t* bar = &s_full[warp][load_stage];
-        if (lane == 0) mbar_arrive_expect_tx(bar, is_k ? k_bytes : v_bytes);
-        __syncwarp();
-        const int in = is_k ? k_in : v_in, row = is_k ? k_row : v_row;
-        if (in >= 0) {
-            uint8_t* dst = ring + load_stage * unit_bytes + lane * R * 128 * halves;
-            const CUtensorMap* map = is_k ? &map_k : &map_v;
-            if (a.merged) {
-                tma_load_4d(dst, map, bar, 0, in, f0 / 64, row);
+            if (is_k) {
+                k_in = next_in;
+                if (k_in >= 0 && (unsigned)next_page >= (unsigned)a.pages) {
+                    record_error(kErrBadIndex);  // its keys are left out
+                    k_in = -1;
+                }
+                k_row = (int)((unsigned)next_page * a.Hkv + ld.hh / a.blocks);
+                const unsigned there = __ballot_sync(0xffffffffu, k_in >= 0);
+                k_bytes = __popc(there) * boxes * box_bytes;
+                const int pos = ld.s * kStep + lane;
+                const unsigned mask =
+                    __ballot_sync(0xffffffffu, pos >= ld.sp.lo && pos < ld.sp.hi && ((there >> (lane / R)) & 1));
+                if (lane == 0) s_mask[warp][k_next & (kMasks - 1)] = mask;
+                if (++k_next < n_steps) {
+                    ld.next(a);
+                    fetch_page();
+                }
             } else {
-                for (int h = 0; h < boxes; ++h) tma_load_3d(dst + h * R * 128, map, bar, f0 + h * 64, in, row);
+                ++v_next;
             }
-        }
-        load_stage = load_stage + 1 == n_units ? 0 : load_stage + 1;
-    };
-    fetch_page();
-    for (int i = 0; i < n_units; ++i) load_next();
+            uint64_t* bar = &s_full[warp][load_stage];
+            if (lane == 0) mbar_arrive_expect_tx(bar, is_k ? k_bytes : v_bytes);
+            __syncwarp();
+            const int in = is_k ? k_in : v_in, row = is_k ? k_row : v_row;
+            if (in >= 0) {
+                uint8_t* dst = ring + load_stage * unit_bytes + lane * R * 128 * halves;
+                const CUtensorMap* map = is_k ? &map_k : &map_v;
+                if (a.merged) {
+                    tma_load_4d(dst, map, bar, 0, in, f0 / 64, row);
+                } else {
+                    for (int h = 0; h < boxes; ++h) tma_load_3d(dst + h * R * 128, map, bar, f0 + h * 64, in, row);
+                }
+            }
+            load_stage = load_stage + 1 == n_units ? 0 : load_stage + 1;
+        };
+        fetch_page();
+        for (int i = 0; i < n_units; ++i) load_next();
 
-    // ---- units in use.  Row r of a unit lies at row_at(r), its second half R rows on; 16-byte
-    // chunks are swizzled by the address's 128-byte line.
-    auto row_at = [&](int r) { return (uint32_t)((r / R) * R * halves + r % R) * 128u; };
-    const uint32_t half_at = R * 128, block_at = row_at(16);  // (16 rows on: a multiple of 1024 bytes)
-    const int k_hi = lane >> 4, v_hi = (lane >> 3) & 1;
-    const uint32_t k_at = row_at(lane & 15), v_at = row_at((lane & 7) + ((lane >> 4) << 3));
-    const uint32_t k_x[2] = {(k_at >> 7) & 7, ((k_at + half_at) >> 7) & 7};
-    const uint32_t v_x[2] = {(v_at >> 7) & 7, ((v_at + half_at) >> 7) & 7};
-    int stage = 0;
-    uint32_t phase = 0;
-    auto wait_unit = [&]() {
-        if (!dead && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][stage], phase, kErrTimeoutLoad))) dead = true;
-        return smem_u32(ring) + stage * unit_bytes;
-    };
-    auto unit_done = [&]() {
-        if (++stage == n_units) {
-            stage = 0;
-            phase ^= 1u;
-        }
-        __syncwarp();  // every lane has read the unit
-        load_next();
-    };
-
-    const int g = lane >> 2, t2 = (lane & 3) * 2;
-    uint32_t qf[kWidth / 16][2];
-    float o[kWidth / 16][4];
-    float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;  // heads t2, t2 + 1
-    float sc[2][4];                                // scores: keys 16 i + g and + 8, heads t2 and t2 + 1
-    uint32_t ph[2][2], pl[2][2], mask = 0;
-    int buf = 0;
-    bool begins = cur.s == cur.sp.s0;
-    Cursor nxt = cur;
-    for (int step = -1; step < n_steps; ++step) {
-        // `cur` is at `step`, `nxt` at the step behind it
-        const bool more = step + 1 < n_steps;
-        const bool ends = step < 0 || cur.s + 1 == cur.sp.s1;  // (an item, or nothing yet)
-        if (more) {
-            if (step >= 0) nxt.next(a);
-            if (ends) {
-                const int heads = heads_of(nxt.hh);
-                const __nv_bfloat16* q = a.q + ((size_t)nxt.b * a.Hq + head0_of(nxt.hh) + min(g, heads - 1)) * a.D + f0;
-#pragma unroll
-                for (int kk = 0; kk < kWidth / 16; ++kk) {
-                    const int x = kk * 16 + t2;
-                    qf[kk][0] = g < heads && x < width ? *reinterpret_cast<const uint32_t*>(q + x) : 0u;
-                    qf[kk][1] = g < heads && x + 8 < width ? *reinterpret_cast<const uint32_t*>(q + x + 8) : 0u;
-                }
-            }
-            const uint32_t base = wait_unit() + k_at;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
-#pragma unroll
-            for (int kk = 0; kk < kWidth / 16; ++kk) {
-                if (W == 0 && kk * 16 >= width) break;
-                const uint32_t at = base + (kk >> 2) * half_at + (((2 * (kk & 3) + k_hi) ^ k_x[kk >> 2]) << 4);
-                uint32_t ka[4], kb[4];
-                ldsm4(at, ka);
-                ldsm4(at + block_at, kb);
-                mma_bf16(sc[0], ka, qf[kk][0], qf[kk][1]);
-                mma_bf16(sc[1], kb, qf[kk][0], qf[kk][1]);
-            }
-            unit_done();
-        }
-        if (step >= 0) {
-            const uint32_t unit = wait_unit();
-            if (mask != ~0u) {
-                // rows without a key hold what the page held (or the ring, where no box was
-                // loaded): p = 0 there must meet a finite value
-                if (!((mask >> lane) & 1)) {
-                    const uint32_t row = unit + row_at(lane);
-                    for (int c = 0; c < halves * 8; ++c)
-                        st_shared_v4(row + (c >> 3) * half_at + (c & 7) * 16, 0, 0, 0, 0);
-                    fence_proxy_async_shared();  // before the ring's next load of these bytes
-                }
-                __syncwarp();
-            }
-            const uint32_t base = unit + v_at;
-#pragma unroll
-            for (int mt = 0; mt < kWidth / 16; ++mt) {
-                if (W == 0 && mt * 16 >= width) break;
-                const uint32_t at = base + (mt >> 2) * half_at + (((2 * (mt & 3) + v_hi) ^ v_x[mt >> 2]) << 4);
-                uint32_t va[4], vb[4];
-                ldsm4_t(at, va);
-                ldsm4_t(at + block_at, vb);
-                mma_bf16(o[mt], va, ph[0][0], ph[0][1]);
-                mma_bf16(o[mt], vb, ph[1][0], ph[1][1]);
-                mma_bf16(o[mt], va, pl[0][0], pl[0][1]);
-                mma_bf16(o[mt], vb, pl[1][0], pl[1][1]);
-            }
-            unit_done();
-            if (ends || !more) {
-                // ---- an item, or a piece of one, is done
-                float s0 = l0, s1 = l1;
-#pragma unroll
-                for (int x = 4; x < 32; x <<= 1) {
-                    s0 += __shfl_xor_sync(0xffffffffu, s0, x);
-                    s1 += __shfl_xor_sync(0xffffffffu, s1, x);
-                }
-                const int heads = heads_of(cur.hh), head0 = head0_of(cur.hh);
-                const bool whole = begins && ends;
-                const float r0 = whole ? (s0 > 0.f ? 1.f / s0 : 0.f) : 1.f;
-                const float r1 = whole ? (s1 > 0.f ? 1.f / s1 : 0.f) : 1.f;
-                const int kind = begins ? 1 : 0;
-                // the last piece of the range may lie in the ring, which is idle then
-                float* part = !more ? reinterpret_cast<float*>(ring) : early0 + warp * early_stride;
-#pragma unroll
-                for (int mt = 0; mt < kWidth / 16; ++mt) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int head = t2 + (e & 1), x = mt * 16 + g + (e >> 1) * 8;
-                        if (head >= heads || x >= width) continue;
-                        const float val = o[mt][e] * ((e & 1) ? r1 : r0);
-                        if (!whole) {
-                            part[head * kSlice + x] = val;
-                        } else {
-                            const size_t at = ((size_t)cur.b * a.Hq + head0 + head) * a.D + f0 + x;
-                            if (a.out_f32) static_cast<float*>(a.out)[at] = val;
-                            else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(val);
-                        }
-                    }
-                }
-                if (w_in == 0 && g == 0) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int head = t2 + e;
-                        if (head >= heads) continue;
-                        const float mm = e ? m1 : m0, ll = e ? s1 : s0;
-                        if (!whole) {
-                            s_ml[team][kind][head] = mm;
-                            s_ml[team][kind][8 + head] = ll;
-                        } else if (a.lse != nullptr) {
-                            a.lse[(size_t)cur.b * a.Hq + head0 + head] =
-                                ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
-                        }
-                    }
-                }
-                if (!whole && w_in == 0 && lane == 0) {
-                    s_has[team][kind] = ends ? 2 : 1;
-                    if (kind == 0) s_end[team] = !more;
-                    s_item[team][kind] =
-                        Item{cur.b, cur.hh, g0 + step - (cur.s - cur.sp.s0), g0 + step + (cur.sp.s1 - 1 - cur.s)};
-                }
-                begins = true;  // (the next step, if any, starts an item)
-            }
-        }
-        if (!more) break;
-        cur = nxt;
-        // ---- whole scores from the team's parts
-        if (kExch && tw > 1) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) exch[buf][warp][i][lane] = make_float4(sc[i][0], sc[i][1], sc[i][2], sc[i][3]);
-            team_sync(team, tw * 32);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float4 s = exch[buf][team * tw][i][lane];
-#pragma unroll
-                for (int w = 1; w < (TW > 0 ? TW : kMaxWarps); ++w) {
-                    if (TW == 0 && w >= tw) break;
-                    const float4 x = exch[buf][team * tw + w][i][lane];
-                    s.x += x.x;
-                    s.y += x.y;
-                    s.z += x.z;
-                    s.w += x.w;
-                }
-                sc[i][0] = s.x;
-                sc[i][1] = s.y;
-                sc[i][2] = s.z;
-                sc[i][3] = s.w;
-            }
-            buf ^= 1;
-        }
-        // ---- running maximum and sum; p in two bf16 parts
-        if (ends) {
-            m0 = m1 = -INFINITY;
-            l0 = l1 = 0.f;
-#pragma unroll
-            for (int mt = 0; mt < kWidth / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
-        }
-        mask = s_mask[warp][(step + 1) & (kMasks - 1)];
-        float n0 = m0, n1 = m1;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[i][e] *= a.scale_log2;
-            if (mask != ~0u) {
-                const bool k0 = (mask >> (16 * i + g)) & 1, k1 = (mask >> (16 * i + g + 8)) & 1;
-                sc[i][0] = k0 ? sc[i][0] : -INFINITY;
-                sc[i][1] = k0 ? sc[i][1] : -INFINITY;
-                sc[i][2] = k1 ? sc[i][2] : -INFINITY;
-                sc[i][3] = k1 ? sc[i][3] : -INFINITY;
-            }
-            n0 = fmaxf(n0, fmaxf(sc[i][0], sc[i][2]));
-            n1 = fmaxf(n1, fmaxf(sc[i][1], sc[i][3]));
-        }
-#pragma unroll
-        for (int x = 4; x < 32; x <<= 1) {
-            n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
-            n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
-        }
-        const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;  // nothing seen yet
-        if (__any_sync(0xffffffffu, n0 != m0 || n1 != m1)) {  // (seldom, after the first steps)
-            const float f0c = ex2f(m0 - b0), f1c = ex2f(m1 - b1);
-            l0 *= f0c;
-            l1 *= f1c;
-#pragma unroll
-            for (int mt = 0; mt < kWidth / 16; ++mt) {
-                o[mt][0] *= f0c;
-                o[mt][1] *= f1c;
-                o[mt][2] *= f0c;
-                o[mt][3] *= f1c;
-            }
-            m0 = n0;
-            m1 = n1;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float p[4] = {ex2f(sc[i][0] - b0), ex2f(sc[i][1] - b1), ex2f(sc[i][2] - b0), ex2f(sc[i][3] - b1)};
-            l0 += p[0] + p[2];
-            l1 += p[1] + p[3];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t h = pack_bf16(p[2 * j], p[2 * j + 1]);
-                pl[i][j] = movm(pack_bf16(p[2 * j] - __uint_as_float(h << 16),
-                                          p[2 * j + 1] - __uint_as_float(h & 0xffff0000u)));
-                ph[i][j] = movm(h);
-            }
-        }
-    }
-    if (dead) {
-        // leave no copy in flight (each wait is bounded again)
-        for (int i = 0; i < n_units; ++i) {
-            mbar_wait(&s_full[warp][stage], phase, kErrTimeoutLoad);
+        // ---- units in use.  Row r of a unit lies at row_at(r), its second half R rows on; 16-byte
+        // chunks are swizzled by the address's 128-byte line.
+        auto row_at = [&](int r) { return (uint32_t)((r / R) * R * halves + r % R) * 128u; };
+        const uint32_t half_at = R * 128, block_at = row_at(16);  // (16 rows on: a multiple of 1024 bytes)
+        const int k_hi = lane >> 4, v_hi = (lane >> 3) & 1;
+        const uint32_t k_at = row_at(lane & 15), v_at = row_at((lane & 7) + ((lane >> 4) << 3));
+        const uint32_t k_x[2] = {(k_at >> 7) & 7, ((k_at + half_at) >> 7) & 7};
+        const uint32_t v_x[2] = {(v_at >> 7) & 7, ((v_at + half_at) >> 7) & 7};
+        int stage = 0;
+        uint32_t phase = 0;
+        auto wait_unit = [&]() {
+            if (!dead && !__all_sync(0xffffffffu, mbar_wait(&s_full[warp][stage], phase, kErrTimeoutLoad))) dead = true;
+            return smem_u32(ring) + stage * unit_bytes;
+        };
+        auto unit_done = [&]() {
             if (++stage == n_units) {
                 stage = 0;
                 phase ^= 1u;
             }
+            __syncwarp();  // every lane has read the unit
+            load_next();
+        };
+
+        const int g = lane >> 2, t2 = (lane & 3) * 2;
+        uint32_t qf[kWidth / 16][2];
+        float o[kWidth / 16][4];
+        float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;  // heads t2, t2 + 1
+        float sc[2][4];                                // scores: keys 16 i + g and + 8, heads t2 and t2 + 1
+        uint32_t ph[2][2], pl[2][2], mask = 0;
+        int buf = 0;
+        bool begins = cur.s == cur.sp.s0;
+        Cursor nxt = cur;
+        for (int step = -1; step < n_steps; ++step) {
+            // `cur` is at `step`, `nxt` at the step behind it
+            const bool more = step + 1 < n_steps;
+            const bool ends = step < 0 || cur.s + 1 == cur.sp.s1;  // (an item, or nothing yet)
+            if (more) {
+                if (step >= 0) nxt.next(a);
+                if (ends) {
+                    const int heads = heads_of(nxt.hh);
+                    const __nv_bfloat16* q = a.q + ((size_t)nxt.b * a.Hq + head0_of(nxt.hh) + min(g, heads - 1)) * a.D + f0;
+#pragma unroll
+                    for (int kk = 0; kk < kWidth / 16; ++kk) {
+                        const int x = kk * 16 + t2;
+                        qf[kk][0] = g < heads && x < width ? *reinterpret_cast<const uint32_t*>(q + x) : 0u;
+                        qf[kk][1] = g < heads && x + 8 < width ? *reinterpret_cast<const uint32_t*>(q + x + 8) : 0u;
+                    }
+                }
+                const uint32_t base = wait_unit() + k_at;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < kWidth / 16; ++kk) {
+                    if (W == 0 && kk * 16 >= width) break;
+                    const uint32_t at = base + (kk >> 2) * half_at + (((2 * (kk & 3) + k_hi) ^ k_x[kk >> 2]) << 4);
+                    uint32_t ka[4], kb[4];
+                    ldsm4(at, ka);
+                    ldsm4(at + block_at, kb);
+                    mma_bf16(sc[0], ka, qf[kk][0], qf[kk][1]);
+                    mma_bf16(sc[1], kb, qf[kk][0], qf[kk][1]);
+                }
+                unit_done();
+            }
+            if (step >= 0) {
+                const uint32_t unit = wait_unit();
+                if (mask != ~0u) {
+                    // rows without a key hold what the page held (or the ring, where no box was
+                    // loaded): p = 0 there must meet a finite value
+                    if (!((mask >> lane) & 1)) {
+                        const uint32_t row = unit + row_at(lane);
+                        for (int c = 0; c < halves * 8; ++c)
+                            st_shared_v4(row + (c >> 3) * half_at + (c & 7) * 16, 0, 0, 0, 0);
+                        fence_proxy_async_shared();  // before the ring's next load of these bytes
+                    }
+                    __syncwarp();
+                }
+                const uint32_t base = unit + v_at;
+#pragma unroll
+                for (int mt = 0; mt < kWidth / 16; ++mt) {
+                    if (W == 0 && mt * 16 >= width) break;
+                    const uint32_t at = base + (mt >> 2) * half_at + (((2 * (mt & 3) + v_hi) ^ v_x[mt >> 2]) << 4);
+                    uint32_t va[4], vb[4];
+                    ldsm4_t(at, va);
+                    ldsm4_t(at + block_at, vb);
+                    mma_bf16(o[mt], va, ph[0][0], ph[0][1]);
+                    mma_bf16(o[mt], vb, ph[1][0], ph[1][1]);
+                    mma_bf16(o[mt], va, pl[0][0], pl[0][1]);
+                    mma_bf16(o[mt], vb, pl[1][0], pl[1][1]);
+                }
+                unit_done();
+                if (ends || !more) {
+                    // ---- an item, or a piece of one, is done
+                    float s0 = l0, s1 = l1;
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1) {
+                        s0 += __shfl_xor_sync(0xffffffffu, s0, x);
+                        s1 += __shfl_xor_sync(0xffffffffu, s1, x);
+                    }
+                    const int heads = heads_of(cur.hh), head0 = head0_of(cur.hh);
+                    const bool whole = begins && ends;
+                    const float r0 = whole ? (s0 > 0.f ? 1.f / s0 : 0.f) : 1.f;
+                    const float r1 = whole ? (s1 > 0.f ? 1.f / s1 : 0.f) : 1.f;
+                    const int kind = begins ? 1 : 0;
+                    // the last piece of the range may lie in the ring, which is idle then
+                    float* part = !more ? reinterpret_cast<float*>(ring) : early0 + warp * early_stride;
+#pragma unroll
+                    for (int mt = 0; mt < kWidth / 16; ++mt) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int head = t2 + (e & 1), x = mt * 16 + g + (e >> 1) * 8;
+                            if (head >= heads || x >= width) continue;
+                            const float val = o[mt][e] * ((e & 1) ? r1 : r0);
+                            if (!whole) {
+                                part[head * kSlice + x] = val;
+                            } else {
+                                const size_t at = ((size_t)cur.b * a.Hq + head0 + head) * a.D + f0 + x;
+                                if (a.out_f32) static_cast<float*>(a.out)[at] = val;
+                                else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(val);
+                            }
+                        }
+                    }
+                    if (w_in == 0 && g == 0) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int head = t2 + e;
+                            if (head >= heads) continue;
+                            const float mm = e ? m1 : m0, ll = e ? s1 : s0;
+                            if (!whole) {
+                                s_ml[team][kind][head] = mm;
+                                s_ml[team][kind][8 + head] = ll;
+                            } else if (a.lse != nullptr) {
+                                a.lse[(size_t)cur.b * a.Hq + head0 + head] =
+                                    ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+                            }
+                        }
+                    }
+                    if (!whole && w_in == 0 && lane == 0) {
+                        s_has[team][kind] = ends ? 2 : 1;
+                        if (kind == 0) s_end[team] = !more;
+                        s_item[team][kind] =
+                            Item{cur.b, cur.hh, g0 + step - (cur.s - cur.sp.s0), g0 + step + (cur.sp.s1 - 1 - cur.s)};
+                    }
+                    begins = true;  // (the next step, if any, starts an item)
+                }
+            }
+            if (!more) break;
+            cur = nxt;
+            // ---- whole scores from the team's parts
+            if (kExch && tw > 1) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) exch[buf][warp][i][lane] = make_float4(sc[i][0], sc[i][1], sc[i][2], sc[i][3]);
+                team_sync(team, tw * 32);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float4 s = exch[buf][team * tw][i][lane];
+#pragma unroll
+                    for (int w = 1; w < (TW > 0 ? TW : kMaxWarps); ++w) {
+                        if (TW == 0 && w >= tw) break;
+                        const float4 x = exch[buf][team * tw + w][i][lane];
+                        s.x += x.x;
+                        s.y += x.y;
+                        s.z += x.z;
+                        s.w += x.w;
+                    }
+                    sc[i][0] = s.x;
+                    sc[i][1] = s.y;
+                    sc[i][2] = s.z;
+                    sc[i][3] = s.w;
+                }
+                buf ^= 1;
+            }
+            // ---- running maximum and sum; p in two bf16 parts
+            if (ends) {
+                m0 = m1 = -INFINITY;
+                l0 = l1 = 0.f;
+#pragma unroll
+                for (int mt = 0; mt < kWidth / 16; ++mt) o[mt][0] = o[mt][1] = o[mt][2] = o[mt][3] = 0.f;
+            }
+            mask = s_mask[warp][(step + 1) & (kMasks - 1)];
+            float n0 = m0, n1 = m1;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[i][e] *= a.scale_log2;
+                if (mask != ~0u) {
+                    const bool k0 = (mask >> (16 * i + g)) & 1, k1 = (mask >> (16 * i + g + 8)) & 1;
+                    sc[i][0] = k0 ? sc[i][0] : -INFINITY;
+                    sc[i][1] = k0 ? sc[i][1] : -INFINITY;
+                    sc[i][2] = k1 ? sc[i][2] : -INFINITY;
+                    sc[i][3] = k1 ? sc[i][3] : -INFINITY;
+                }
+                n0 = fmaxf(n0, fmaxf(sc[i][0], sc[i][2]));
+                n1 = fmaxf(n1, fmaxf(sc[i][1], sc[i][3]));
+            }
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) {
+                n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, x));
+                n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, x));
+            }
+            const float b0 = n0 == -INFINITY ? 0.f : n0, b1 = n1 == -INFINITY ? 0.f : n1;  // nothing seen yet
+            if (__any_sync(0xffffffffu, n0 != m0 || n1 != m1)) {  // (seldom, after the first steps)
+                const float f0c = ex2f(m0 - b0), f1c = ex2f(m1 - b1);
+                l0 *= f0c;
+                l1 *= f1c;
+#pragma unroll
+                for (int mt = 0; mt < kWidth / 16; ++mt) {
+                    o[mt][0] *= f0c;
+                    o[mt][1] *= f1c;
+                    o[mt][2] *= f0c;
+                    o[mt][3] *= f1c;
+                }
+                m0 = n0;
+                m1 = n1;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float p[4] = {ex2f(sc[i][0] - b0), ex2f(sc[i][1] - b1), ex2f(sc[i][2] - b0), ex2f(sc[i][3] - b1)};
+                l0 += p[0] + p[2];
+                l1 += p[1] + p[3];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t h = pack_bf16(p[2 * j], p[2 * j + 1]);
+                    pl[i][j] = movm(pack_bf16(p[2 * j] - __uint_as_float(h << 16),
+                                              p[2 * j + 1] - __uint_as_float(h & 0xffff0000u)));
+                    ph[i][j] = movm(h);
+                }
+            }
+        }
+        if (dead) {
+            // leave no copy in flight (each wait is bounded again)
+            for (int i = 0; i < n_units; ++i) {
+                mbar_wait(&s_full[warp][stage], phase, kErrTimeoutLoad);
+                if (++stage == n_units) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
         }
     }
-    }  // n_steps > 0
 
     // requests without keys: their output is zero
 #pragma unroll 1

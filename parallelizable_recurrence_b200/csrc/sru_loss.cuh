@@ -19,8 +19,11 @@
 // tile's exponentials.
 // The gradients run over pieces of the vocabulary, so that dz never takes more
 // than a bounded buffer; z is recomputed there (2 M V K operations on top of
-// the gradients' 4 M V K), since reading it back in fp32 and writing it costs
-// more than the product for K up to about 2000.
+// the gradients' 4 M V K): kept, it would take 4 M V bytes (2 GB at M16384 V32000),
+// and writing and reading it as long as the product at K of about 900.
+// Measured, a kernel alone: M16384 V32000, kStats 702 us at K1024 (1.53 PFLOP/s) and
+// 1.36 ms at K2048 (1.58); M4096 V8192 K1024, kStats 53 us (1.30), both gradient
+// products 98.5 us (1.40).  In a row, long calls settle at the card's power limit.
 #pragma once
 
 #include <type_traits>
@@ -315,7 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + W * 32, 1)
 // between them.  A unit is an output tile and one k part of it.  (Tiles of 128
 // columns for a K that fills its last 256 badly were slower: 12% at K520.)
 struct GradProblem {
-    int units, n_tiles, splits, kblocks, kper, slab_rows, rows;  // rows: of the output
+    int units, n_tiles, splits, kblocks, kper, slab_rows;
     int bf16, add;  // output type; add onto the output (fp32)
 };
 struct GradArgs {
