@@ -2180,18 +2180,21 @@ sru_status sru_attention_decode(const void* q, const void* k_cache, const void* 
     const size_t smem = rings + (fits ? early : 0);
     a.early_floats = fits ? (int)(early / sizeof(float)) / (p.tw * p.teams) : 0;
     using sru::cache::cache_attention_kernel;
-    // any D, or a form without loops over the width (B64 H2 len <= 4000: D64 33 -> 27.5 us, D384
-    // 100 -> 82, D768 193 -> 160)
+    // any D, or, for 64 and the multiples of 128, a form without loops over the width (B64 H2
+    // len <= 4000: D64 33 -> 27.5 us, D384 100 -> 82, D768 193 -> 160)
     auto kern = cache_attention_kernel<0, 0>;
-    switch (D) {
-        case 64: kern = cache_attention_kernel<1, 64>; break;
-        case 128: kern = cache_attention_kernel<1, 128>; break;
-        case 256: kern = cache_attention_kernel<2, 128>; break;
-        case 384: kern = cache_attention_kernel<3, 128>; break;
-        case 512: kern = cache_attention_kernel<4, 128>; break;
-        case 768: kern = cache_attention_kernel<6, 128>; break;
-        case 1024: kern = cache_attention_kernel<8, 128>; break;
-        default: break;
+    if (D == 64) kern = cache_attention_kernel<1, 64>;
+    if (D % 128 == 0) {
+        switch (p.tw) {
+            case 1: kern = cache_attention_kernel<1, 128>; break;
+            case 2: kern = cache_attention_kernel<2, 128>; break;
+            case 3: kern = cache_attention_kernel<3, 128>; break;
+            case 4: kern = cache_attention_kernel<4, 128>; break;
+            case 5: kern = cache_attention_kernel<5, 128>; break;
+            case 6: kern = cache_attention_kernel<6, 128>; break;
+            case 7: kern = cache_attention_kernel<7, 128>; break;
+            default: kern = cache_attention_kernel<8, 128>; break;
+        }
     }
     SRU_CUDA_TRY(ensure_smem(reinterpret_cast<const void*>(kern), most));
     // The caches as (D, page_size, pages * Hkv), in boxes of 64 features x box_rows rows of

@@ -256,7 +256,7 @@ EDGES = [0, 1, 15, 16, 17, 31, 33, 0, 100]
 
 @pytest.mark.parametrize("Hq,Hkv,D,ps", [
     (1, 1, 8, 16), (1, 1, 64, 16), (2, 2, 72, 1), (8, 1, 128, 32), (9, 3, 128, 24), (6, 2, 136, 7), (9, 1, 64, 100),
-    (1, 1, 256, 16), (16, 1, 192, 16), (40, 2, 96, 8), (1, 1, 384, 64), (3, 1, 512, 16), (5, 1, 640, 48),
+    (1, 1, 256, 16), (16, 1, 192, 16), (40, 2, 96, 8), (1, 1, 384, 64), (3, 1, 512, 16), (5, 1, 640, 48), (1, 1, 320, 16), (4, 2, 896, 16),
     (2, 1, 768, 16), (2, 2, 904, 5), (1, 1, 1024, 16), (17, 1, 1024, 32),
 ])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
@@ -353,6 +353,45 @@ def test_one_workspace_for_calls_of_any_shape_and_two_graphs(sru):
     assert sru.sru_sync_status() == 0
     for k in (0, 3):
         _check_decode(outs[k], None, inputs[k][0], inputs[k][5], inputs[k][6], inputs[k][0].shape[2] ** -0.5, 0)
+
+
+def test_captured_between_copies_and_joined_streams(sru):
+    """Captured calls whose predecessors are a copy, a fill, another stream's kernel and a
+    kernel of the library, replayed on new data."""
+    q, kc, vc, table, lengths, K, V = _decode_inputs(3, 2, 1, 256, [400, 77, 0], 16, seed=5)
+    T, ps = 5, 16
+    src, rows = torch.randn(3, 2, 256, device="cuda").bfloat16(), torch.randn(T, 1, 256, device="cuda").bfloat16()
+    slots = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    out, out2, out3 = (torch.empty(3, 2, 256, device="cuda") for _ in range(3))
+    qq = torch.zeros_like(q)
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        qq.copy_(src)                                                    # a copy
+        sru.sru_attention_decode(qq, kc, vc, table, lengths, out)
+        out2.zero_()                                                     # a fill
+        sru.sru_attention_decode(qq, kc, vc, table, lengths, out2)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            sru.sru_cache_append(rows, rows, slots, kc, vc)              # another stream, joined
+        main.wait_stream(side)
+        sru.sru_attention_decode(qq, kc, vc, table, lengths, out3)
+        qq.add_(1)                                                       # a kernel that writes what was read
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2):
+        src.copy_(torch.randn(src.shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda"))
+        for o in (out, out2, out3):
+            o.fill_(float("nan"))
+        graph.replay()
+        assert sru.sru_sync_status() == 0
+        for o in (out, out2, out3):
+            _check_decode(o, None, src, K, V, 1 / 16, 0)
 
 
 def test_calls_one_after_another_without_a_wait(sru):
