@@ -1933,9 +1933,12 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
     a.V = V;
     float* scale = reinterpret_cast<float*>(ws + p.scale_off);
     a.scale = scale;
-    s = launch_overlapped(sru::loss::loss_scale_kernel, dim3(1), 1024, 0, st, dloss, a.targets, scale, (int)M,
-                          (long long)V);
-    if (s != SRU_OK) return s;
+    a.inline_scale = M <= sru::loss::kInlineScaleRows;
+    if (!a.inline_scale) {
+        s = launch_overlapped(sru::loss::loss_scale_kernel, dim3(1), 1024, 0, st, dloss, a.targets, scale, (int)M,
+                              (long long)V);
+        if (s != SRU_OK) return s;
+    }
     // dH is summed over the pieces in fp32: in place, or in the workspace when it is split
     // along the vocabulary or leaves as bf16
     const bool h_in_slabs = p.dh.splits > 1 || (p.pieces > 1 && dh_t == SRU_BF16);

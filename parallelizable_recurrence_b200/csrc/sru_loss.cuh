@@ -65,13 +65,36 @@ __device__ __forceinline__ void unit_tile(int u, int m_tiles, int n_tiles, int& 
     tm = g * kGroupM + r - tn * gm;
 }
 
+// The largest weight of a counted row (1 if there is none, or no finite one).  dz is
+// held over it, and the gradients are multiplied by it in fp32: with the usual equal
+// weights 1 / n, every dz of a target is then p - 1 rounded to bf16, whose error
+// differs from row to row, and not -1 / n, whose error would be the same in all
+// rows and scale the whole gradient by up to 2^-9.
+// Here by one warp, rows 32 apart per lane; few enough rows (kInlineScaleRows) that
+// the epilogue warps have it before their first tile is multiplied.
+constexpr int kInlineScaleRows = 1024;
+__device__ __forceinline__ float counted_weight(const float* dloss, const long long* targets, int i, long long V) {
+    const long long t = targets[i];
+    const float g = fabsf(dloss[i]);
+    return t >= 0 && t < V && g < INFINITY ? g : 0.f;
+}
+__device__ __forceinline__ float weight_scale(const float* dloss, const long long* targets, int M, long long V) {
+    float top = 0.f;
+#pragma unroll 8
+    for (int i = threadIdx.x & 31; i < M; i += 32) top = fmaxf(top, counted_weight(dloss, targets, i, V));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    return top > 0.f ? top : 1.f;
+}
+
 struct LossArgs {
     const long long* targets;  // (M): the class of each row; negative = not counted
     float2* partial;           // kStats: (parts of tiles, M) maximum and sum of exponentials
     float* target_logit;       // kStats: (M)
     const float* lse;          // kGrad: (M)
     const float* dloss;        // kGrad: (M)
-    const float* scale;        // kGrad: dz is taken over it (see loss_scale_kernel)
+    float* scale;              // kGrad: dz is taken over it; written here when inline_scale
+    int inline_scale;
     long long v0, V;           // first column of this piece of the vocabulary, its whole size
 };
 
@@ -212,7 +235,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + W * 32, 1)
         uint8_t* bufs = epi + (size_t)(warp - 2) * kBufs * P_EPI_BUF;
         int it = 0;
         uint32_t nstaged = 0;
-        const float scale = EPI == kGrad ? *a.scale : 1.f;
+        float scale = 1.f;
+        if (EPI == kGrad) {
+            scale = a.inline_scale ? weight_scale(a.dloss, a.targets, M, a.V) : *a.scale;
+            if (a.inline_scale && blockIdx.x == 0 && warp == 2 && lane == 0) *a.scale = scale;
+        }
         for (int u = pair_id; u < units; u += n_pairs, ++it) {
             int tm, tn;
             unit_tile(u, m_tiles, n_tiles, tm, tn);
@@ -570,11 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
 }
 
-// The largest weight of a counted row (1 if there is none, or no finite one).  dz is
-// held over it, and the gradients are multiplied by it in fp32: with the usual equal
-// weights 1 / n, every dz of a target is then p - 1 rounded to bf16, whose error
-// differs from row to row, and not -1 / n, whose error would be the same in all
-// rows and scale the whole gradient by up to 2^-9.
+// The same over many rows, in a launch of its own.
 __global__ void __launch_bounds__(1024) loss_scale_kernel(const float* __restrict__ dloss,
                                                           const long long* __restrict__ targets,
                                                           float* __restrict__ scale, int M, long long V) {
@@ -583,11 +606,7 @@ __global__ void __launch_bounds__(1024) loss_scale_kernel(const float* __restric
     pdl_wait();
     float top = 0.f;
 #pragma unroll 4
-    for (int i = threadIdx.x; i < M; i += 1024) {
-        const long long t = targets[i];
-        const float g = fabsf(dloss[i]);
-        if (t >= 0 && t < V && g < INFINITY) top = fmaxf(top, g);
-    }
+    for (int i = threadIdx.x; i < M; i += 1024) top = fmaxf(top, counted_weight(dloss, targets, i, V));
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
