@@ -243,9 +243,10 @@ __global__ void __launch_bounds__(256) cache_slots_kernel(ExtendArgs a) {
         const int first = a.offsets[b], n = a.offsets[b + 1] - first;
         if (n <= kExtDirect || t == first) continue;
         int s = -1;
-        if (a.slots[first] >= 0) {
+        // (offsets that wrapped, from 2^31 tokens in one step, lead outside neither array)
+        if ((unsigned)first < (unsigned)a.T && a.slots[first] >= 0) {
             const int pos = a.lengths_out[b] - n + (t - first), p = pos / a.ps;
-            const int page = a.table[(size_t)b * a.maxp + p];
+            const int page = pos >= 0 && p < a.maxp ? a.table[(size_t)b * a.maxp + p] : -1;
             if (page >= 0) s = page * a.ps + (pos - p * a.ps);
         }
         a.slots[t] = s;

@@ -149,6 +149,25 @@ def test_extend_of_no_requests_and_of_no_rows(sru):
     _check_extend(sru, [3, 3], [0, -1], [[0], [1]], [-1, -1], 0, 4, 0)
 
 
+@pytest.mark.parametrize("T", [600, 5000])
+def test_extend_with_too_many_tokens_stays_inside_its_arrays(sru, T):
+    """Tokens from 2^31 on wrap the offsets: what the step grants is unspecified, what lies around its arrays untouched."""
+    big, ps, B, maxp = 2**31 - 1, 8, 6, 700
+    whole = {n: torch.full((64 + size + 64,), -7, dtype=torch.int32, device="cuda")
+             for n, size in (("table", B * maxp), ("slots", T), ("offsets", B + 1), ("free", B * maxp), ("out", B))}
+    part = {n: w[64:-64] for n, w in whole.items()}
+    for new in ([big, 10, big, 300, 10, 5], [5, big, 300, 2, big, 300], [big] * B, [-1, big, big, 300, -1, 90]):
+        part["free"].copy_(torch.arange(B * maxp))
+        n = _i32([B * maxp])
+        sru.sru_cache_extend(_i32([0] * B), _i32(new), part["table"].view(B, maxp), part["free"], n, ps, part["out"], n,
+                             part["offsets"], part["slots"])
+        assert sru.sru_sync_status() == 0
+        assert int(part["slots"].max()) < B * maxp * ps and 0 <= int(n) <= B * maxp
+        for name, w in whole.items():
+            assert (w[:64] == -7).all() and (w[-64:] == -7).all(), name
+    _check_extend(sru, [3, 3], [0, -1], [[0], [1]], [-1, -1], 0, 4, 0)
+
+
 # ----------------------------------------------------------------------- append
 @pytest.mark.parametrize("T,H,D,ps", [(1, 1, 8, 1), (5, 3, 72, 7), (300, 8, 128, 16), (70, 1, 1024, 64)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
