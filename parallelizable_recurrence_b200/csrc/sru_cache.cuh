@@ -257,11 +257,12 @@ __global__ void __launch_bounds__(256) cache_slots_kernel(ExtendArgs a) {
 // Row r of K and V (T rows of Hkv * D elements, k_ld / v_ld apart) to slot
 // slots[r] of the caches, rounded to bf16; a negative slot writes nothing.  Pure
 // copy, bound by memory: 16-byte items, four in flight per thread (16384 rows of K and
-// V, d' 512: 67 MB in 12.1 us, 5.6 TB/s; one item per thread: 18.6 us).
+// V, d' 512: 67 MB in 12.1 us, 5.6 TB/s; one item per thread: 18.6 us).  Plain loads: the
+// kernels before it may still write rows and slots when it starts.
 template <typename SrcT>
 __device__ __forceinline__ uint4 load8_bf16(const SrcT* p) {
-    if (sizeof(SrcT) == 2) return __ldg(reinterpret_cast<const uint4*>(p));
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    if (sizeof(SrcT) == 2) return *reinterpret_cast<const uint4*>(p);
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
     __nv_bfloat162 w[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w),
                            __floats2bfloat162_rn(b.x, b.y), __floats2bfloat162_rn(b.z, b.w)};
     return *reinterpret_cast<uint4*>(w);
@@ -269,9 +270,8 @@ __device__ __forceinline__ uint4 load8_bf16(const SrcT* p) {
 constexpr int kAppendItems = 4;  // 16-byte stores per thread, their loads issued together
 template <typename SrcT>
 __global__ void __launch_bounds__(256)
-    cache_append_kernel(const SrcT* __restrict__ K, long long k_ld, const SrcT* __restrict__ V, long long v_ld,
-                        const int* __restrict__ slots, __nv_bfloat16* __restrict__ k_cache,
-                        __nv_bfloat16* __restrict__ v_cache, unsigned items, int Hkv, int D, int ps,
+    cache_append_kernel(const SrcT* K, long long k_ld, const SrcT* V, long long v_ld, const int* slots,
+                        __nv_bfloat16* k_cache, __nv_bfloat16* v_cache, unsigned items, int Hkv, int D, int ps,
                         long long n_slots) {
     pdl_launch();
     pdl_wait();
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(256)
         if (i < items && i >= i0) {
             const unsigned r = i / per_row;
             col[k] = i - r * per_row;
-            slot[k] = __ldg(slots + r);
+            slot[k] = slots[r];
             v[k] = load8_bf16(src + r * ld + (long long)col[k] * 8);
         }
     }

@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
             next_in = -1;
             if (lane < groups && pos + R > ld.sp.lo && pos < ld.sp.hi) {
                 const int p = pos / a.ps;
-                next_page = __ldg(a.table + (size_t)ld.b * a.maxp + p);
+                next_page = a.table[(size_t)ld.b * a.maxp + p];
                 next_in = pos - p * a.ps;
             }
         };

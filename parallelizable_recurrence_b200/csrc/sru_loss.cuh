@@ -598,9 +598,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 }
 
 // The same over many rows, in a launch of its own.
-__global__ void __launch_bounds__(1024) loss_scale_kernel(const float* __restrict__ dloss,
-                                                          const long long* __restrict__ targets,
-                                                          float* __restrict__ scale, int M, long long V) {
+__global__ void __launch_bounds__(1024) loss_scale_kernel(const float* dloss, const long long* targets, float* scale,
+                                                          int M, long long V) {
     __shared__ float part[32];
     pdl_launch();
     pdl_wait();
@@ -623,9 +622,8 @@ __global__ void __launch_bounds__(1024) loss_scale_kernel(const float* __restric
 // tile groups per CTA (consecutive threads read consecutive rows).
 constexpr int kJoinRows = 32, kJoinGroups = 32;
 __global__ void __launch_bounds__(kJoinRows* kJoinGroups)
-    vocab_loss_kernel(const float2* __restrict__ partial, const float* __restrict__ target_logit,
-                      const long long* __restrict__ targets, float* __restrict__ loss, float* __restrict__ lse,
-                      int M, int parts, long long V) {
+    vocab_loss_kernel(const float2* partial, const float* target_logit, const long long* targets, float* loss,
+                      float* lse, int M, int parts, long long V) {
     __shared__ float2 part[kJoinGroups][kJoinRows + 1];
     pdl_launch();
     pdl_wait();
@@ -656,8 +654,8 @@ __global__ void __launch_bounds__(kJoinRows* kJoinGroups)
 // out[r][c] = sum over s = 0, 1, .. of slabs[s * slab_rows + r][c] in that order,
 // four columns per thread (C % 4 == 0).
 template <typename OutT>
-__global__ void __launch_bounds__(256) slab_sum_kernel(const float4* __restrict__ slabs, OutT* __restrict__ out,
-                                                       int R, int C4, long long slab_rows, int splits) {
+__global__ void __launch_bounds__(256) slab_sum_kernel(const float4* slabs, OutT* out, int R, int C4,
+                                                       long long slab_rows, int splits) {
     pdl_launch();
     pdl_wait();
     const size_t n = (size_t)R * C4;

@@ -251,6 +251,8 @@ __device__ __forceinline__ void tc_commit_pair_mc(uint64_t* bar, uint16_t cta_ma
 // ---- programmatic dependent launch: the next kernel on the stream, if launched
 // so, may begin its prologue once every CTA of this one has called pdl_launch (or
 // left); its pdl_wait returns when this kernel has completed and its writes are visible.
+// The next kernel so starts before its inputs are written: none of its loads may take the
+// read-only path (__ldg, const __restrict__), which is for data that no longer changes.
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -1,0 +1,101 @@
+"""Calls of the paged cache and of the vocabulary loss among other calls: one after another without a
+wait, each reading what the one before it wrote.  Every result must have the bits that the same
+call gives when each call is waited for.
+"""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_cache import _extend_reference, _i32
+from test_gpu_loss import _inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sru():
+    import parallelizable_recurrence_b200 as m
+    m.load_library()
+    return m
+
+
+# B requests, rows per step; the second has the rows kernel behind the bookkeeping and long runs of slots
+@pytest.mark.parametrize("B,maxp,T,most", [(24, 8, 64, 3), (40, 30, 2500, 60)])
+def test_serving_calls_in_a_row_read_what_was_just_written(sru, B, maxp, T, most):
+    """Extend, append and attend on the same buffers, whose contents change at every step."""
+    Hq, Hkv, D, ps, steps = 4, 2, 128, 8, 24
+    pages = B * maxp
+    rng = np.random.default_rng(B)
+    adds = rng.integers(0, most + 1, (steps, B))
+    adds[rng.random((steps, B)) < 0.05] = -1
+    order = rng.permutation(pages)
+    g = torch.Generator(device="cuda").manual_seed(B)
+    new = _i32(adds)
+    KV = torch.randn(steps, T, 2, Hkv, D, generator=g, device="cuda").bfloat16()
+    q = torch.randn(steps, B, Hq, D, generator=g, device="cuda").bfloat16()
+    ws = torch.empty(sru.sru_attention_decode_workspace_bytes(B, Hq, Hkv, D), dtype=torch.uint8, device="cuda")
+
+    def serve(wait):
+        lengths = torch.zeros(B, dtype=torch.int32, device="cuda")
+        table = torch.full((B, maxp), -1, dtype=torch.int32, device="cuda")
+        free, count = _i32(order), _i32([pages])
+        offsets, slots = torch.zeros_like(_i32(range(B + 1))), torch.zeros(T, dtype=torch.int32, device="cuda")
+        kc = torch.zeros(pages, Hkv, ps, D, device="cuda", dtype=torch.bfloat16)
+        vc = torch.zeros_like(kc)
+        out = torch.zeros(steps, B, Hq, D, device="cuda", dtype=torch.bfloat16)
+        torch.cuda.synchronize()
+        for i in range(steps):
+            sru.sru_cache_extend(lengths, new[i], table, free, count, ps, lengths, count, offsets, slots)
+            if wait:
+                torch.cuda.synchronize()
+            sru.sru_cache_append(KV[i, :, 0], KV[i, :, 1], slots, kc, vc)
+            if wait:
+                torch.cuda.synchronize()
+            sru.sru_attention_decode(q[i], kc, vc, table, lengths, out[i], workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+        assert sru.sru_sync_status() == 0
+        return lengths, table, free, count, offsets, slots, kc, vc, out
+
+    want = serve(True)
+    for _ in range(3):
+        for got, ref in zip(serve(False), want):
+            assert torch.equal(got, ref)
+    # the bookkeeping and the caches by the definition, too
+    n, table, free, count = [0] * B, [[-1] * maxp for _ in range(B)], order.tolist(), pages
+    kc = torch.zeros(pages, Hkv, ps, D, device="cuda", dtype=torch.bfloat16)
+    for i in range(steps):
+        table, free, n, count, offsets, slots, _ = _extend_reference(n, adds[i].tolist(), table, free, count, ps, T)
+        at = torch.tensor(slots, device="cuda")
+        there = at >= 0
+        kc[at[there] // ps, :, at[there] % ps] = KV[i, there, 0]
+    assert want[0].tolist() == n and int(want[3]) == count and want[5].tolist() == slots
+    assert torch.equal(want[6], kc)
+
+
+def test_losses_in_a_row_read_what_was_just_written(sru):
+    """Losses and gradients of several batches through the same buffers, the workspace
+    shared, each gradient the rows of the next loss."""
+    M, V, K = 1100, 2000, 128
+    H, W, t, w = _inputs(M, V, K, seed=6)
+    ws = torch.empty(sru.sru_softmax_loss_workspace_bytes(M, V, K), dtype=torch.uint8, device="cuda")
+
+    def steps(wait):
+        rows = [H.clone(), torch.empty_like(H)]
+        loss, lse = torch.zeros(6, M, device="cuda"), torch.zeros(6, M, device="cuda")
+        dW = torch.zeros(6, V, K, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(6):
+            sru.sru_softmax_loss(rows[i % 2], W, t, loss[i], lse[i], workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+            sru.sru_softmax_loss_backward(rows[i % 2], W, t, lse[i], w, rows[(i + 1) % 2], dW[i], workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+        assert sru.sru_sync_status() == 0
+        return loss, lse, dW, rows[0]
+
+    want = steps(True)
+    for _ in range(3):
+        for got, ref in zip(steps(False), want):
+            assert torch.equal(got, ref)
