@@ -431,13 +431,14 @@ def _call(fn, device: int, stream, *args):
 
 
 def _scratch(nbytes: int, device: int, stream) -> Optional[torch.Tensor]:
-    """A workspace for one call: torch reuses it only after the call's stream has passed it."""
+    """A workspace for one call, freed when the call returns.  Its block comes from the call's own stream, which
+    alone may be given it again while the call runs."""
     if nbytes == 0:
         return None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
-    if stream is not None and stream != torch.cuda.current_stream(device):
-        ws.record_stream(stream)
-    return ws
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
 
 
 def sru_softmax_loss_workspace_bytes(M: int, V: int, K: int, backward: bool = True) -> int:

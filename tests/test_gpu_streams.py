@@ -1,12 +1,12 @@
 """Calls of the paged cache and of the vocabulary loss among other calls: one after another without a
-wait, each reading what the one before it wrote.  Every result must have the bits that the same
-call gives when each call is waited for.
+wait, each reading what the one before it wrote, and two at once on two streams.  Every result
+must have the bits that the same call gives when each call is waited for.
 """
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_cache import _extend_reference, _i32
+from test_gpu_cache import _decode_inputs, _extend_reference, _i32
 from test_gpu_loss import _inputs
 
 pytestmark = pytest.mark.gpu
@@ -99,3 +99,60 @@ def test_losses_in_a_row_read_what_was_just_written(sru):
     for _ in range(3):
         for got, ref in zip(steps(False), want):
             assert torch.equal(got, ref)
+
+
+def _at_once(sru, first, second):
+    """first on the current stream, then second on another one while it runs; and the other way round."""
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for a, b in ((first, second), (second, first)):
+        for _ in range(3):
+            side.wait_stream(torch.cuda.current_stream())
+            a(stream=None)
+            b(stream=side)
+            a(stream=None)
+            b(stream=side)
+            torch.cuda.current_stream().wait_stream(side)
+    assert sru.sru_sync_status() == 0
+
+
+def test_losses_without_a_workspace_on_two_streams_at_once(sru):
+    sizes = [(2048, 20000, 512), (2048, 19000, 512)]
+    calls, got, want = [], [], []
+    for i, (M, V, K) in enumerate(sizes):
+        H, W, t, w = _inputs(M, V, K, seed=i)
+        out = [torch.empty(M, device="cuda"), torch.empty(M, device="cuda"), torch.empty(M, K, device="cuda"),
+               torch.empty(V, K, device="cuda")]
+
+        def call(stream, H=H, W=W, t=t, w=w, out=out):
+            sru.sru_softmax_loss(H, W, t, out[0], out[1], stream=stream)
+            sru.sru_softmax_loss_backward(H, W, t, out[1], w, out[2], out[3], stream=stream)
+
+        call(None)
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in out])
+        calls.append(call)
+        got.append(out)
+    _at_once(sru, *calls)
+    for a, b in zip(sum(got, []), sum(want, [])):
+        assert torch.equal(a, b)
+
+
+def test_attention_without_a_workspace_on_two_streams_at_once(sru):
+    # (long, and every request in pieces that cross the CTAs' borders)
+    calls, got, want = [], [], []
+    for i, lengths in enumerate(([7001] * 21, [6500] * 23)):
+        q, kc, vc, table, lengths, _, _ = _decode_inputs(len(lengths), 1, 1, 1024, lengths, 16, seed=i)
+        out = torch.empty(q.shape, device="cuda")
+
+        def call(stream, q=q, kc=kc, vc=vc, table=table, lengths=lengths, out=out):
+            sru.sru_attention_decode(q, kc, vc, table, lengths, out, stream=stream)
+
+        call(None)
+        torch.cuda.synchronize()
+        want.append(out.clone())
+        calls.append(call)
+        got.append(out)
+    _at_once(sru, *calls)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
