@@ -164,6 +164,17 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _scratch(nbytes: int, device, stream) -> Optional[torch.Tensor]:
+    """A workspace for one call, freed when the call returns.  Its block comes from the call's own stream, which
+    alone may be given it again while the call runs."""
+    if nbytes == 0:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _check(status: int, where: str):
     if status != SRU_OK:
         raise SRUError(status, where, _lib)
@@ -295,8 +306,8 @@ def sru_project_factored_backward(dU, X, Wq, Wo, P, dP, dX=None, accumulate: boo
     Kp, N = Wq.shape[0], Wo.shape[0]
     if workspace is None:
         n = int(lib.sru_project_factored_backward_workspace_bytes(M, N, K, Kp))
-        workspace = torch.empty(n, dtype=torch.uint8, device=dU.device)
-    ws_ptr = _ptr(workspace) if workspace.numel() > 0 else None
+        workspace = _scratch(n, dU.device, stream)
+    ws_ptr = _ptr(workspace) if _nbytes(workspace) > 0 else None
     _check(lib.sru_project_factored_backward(_ptr(dU, torch.bfloat16), _ptr(X, torch.bfloat16),
                                              _ptr(Wq, torch.bfloat16), _ptr(Wo, torch.bfloat16),
                                              _ptr(P, torch.bfloat16), _ptr(dP, torch.bfloat16),
@@ -322,7 +333,7 @@ def sru_attention_project(X, Wq, Wkv, Wo, U, L: int, B: int, alpha: float, ln_ga
         n = int(lib.sru_attention_workspace_bytes(L, B, dp))
         if n == 0:
             raise SRUError(SRU_ERR_UNSUPPORTED, "sru_attention_workspace_bytes", lib)
-        workspace = torch.empty(n, dtype=torch.uint8, device=X.device)
+        workspace = _scratch(n, X.device, stream)
     _check(lib.sru_attention_project(_ptr(X, torch.bfloat16), _ptr(Wq, torch.bfloat16), _ptr(Wkv, torch.bfloat16),
                                      _ptr(Wo, torch.bfloat16), float(alpha), _ptr(ln_gamma, torch.float32),
                                      _ptr(ln_beta, torch.float32), int(bool(causal)), _ptr(U), _dtype_code(U),
@@ -353,7 +364,7 @@ def sru_attention_project_backward(dU, X, Wq, Wkv, Wo, L: int, B: int, alpha: fl
         n = int(lib.sru_attention_backward_workspace_bytes(L, B, d, dp, N))
         if n == 0:
             raise SRUError(SRU_ERR_UNSUPPORTED, "sru_attention_backward_workspace_bytes", lib)
-        workspace = torch.empty(n, dtype=torch.uint8, device=X.device)
+        workspace = _scratch(n, X.device, stream)
     _check(lib.sru_attention_project_backward(
         _ptr(dU, torch.bfloat16), _ptr(X, torch.bfloat16), _ptr(Wq, torch.bfloat16), _ptr(Wkv, torch.bfloat16),
         _ptr(Wo, torch.bfloat16), float(alpha), _ptr(ln_gamma, torch.float32), _ptr(ln_beta, torch.float32),
@@ -376,9 +387,7 @@ def sru_decode_step(X_t, W, x_t, v, b, c, h_t, alpha: float = 1.0, workspace=Non
     if W.shape[0] != 3 * d or W.shape[1] != d:
         raise ValueError("W must be (3*d, d)")
     if workspace is None:
-        n = int(lib.sru_decode_workspace_bytes(B, d))
-        if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=X_t.device)
+        workspace = _scratch(int(lib.sru_decode_workspace_bytes(B, d)), X_t.device, stream)
     _check(lib.sru_decode_step(_ptr(X_t, torch.bfloat16), _ptr(W, torch.bfloat16), _ptr(x_t, torch.float32),
                                _ptr(v, torch.float32), _ptr(b, torch.float32), _ptr(c, torch.float32),
                                _ptr(h_t, torch.float32), B, d, float(alpha), _ptr(workspace), _nbytes(workspace),
@@ -428,17 +437,6 @@ def _call(fn, device: int, stream, *args):
             status = fn(*args, handle)
     if status != SRU_OK:
         raise SRUError(status, fn.__name__, _lib)
-
-
-def _scratch(nbytes: int, device: int, stream) -> Optional[torch.Tensor]:
-    """A workspace for one call, freed when the call returns.  Its block comes from the call's own stream, which
-    alone may be given it again while the call runs."""
-    if nbytes == 0:
-        return None
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", device))
 
 
 def sru_softmax_loss_workspace_bytes(M: int, V: int, K: int, backward: bool = True) -> int:

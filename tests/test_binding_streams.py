@@ -69,6 +69,16 @@ CALLS = {
         **kw),
     "sru_attention_decode": lambda **kw: sru.sru_attention_decode(
         _bf(3, 4, 64), _bf(4, 2, 16, 64), _bf(4, 2, 16, 64), _i32(3, 2), _i32(3), _bf(3, 4, 64), **kw),
+    "sru_project_factored_backward": lambda **kw: sru.sru_project_factored_backward(
+        _bf(6, 24), _bf(6, 8), _bf(4, 8), _bf(24, 4), _bf(6, 4), _bf(6, 4), **kw),
+    "sru_attention_project": lambda **kw: sru.sru_attention_project(
+        _bf(6, 8), _bf(4, 8), _bf(8, 4), _bf(24, 4), _bf(6, 24), 3, 2, 1.0, **kw),
+    "sru_attention_project_backward": lambda **kw: sru.sru_attention_project_backward(
+        _bf(6, 24), _bf(6, 8), _bf(4, 8), _bf(8, 4), _bf(24, 4), 3, 2, 1.0, _bf(8), torch.zeros(6, 8),
+        torch.zeros(4, 8), torch.zeros(8, 4), torch.zeros(24, 4), **kw),
+    "sru_decode_step": lambda **kw: sru.sru_decode_step(
+        _bf(8, 8), _bf(24, 8), torch.zeros(8, 8), torch.zeros(2, 8), torch.zeros(2, 8), torch.zeros(8, 8),
+        torch.zeros(8, 8), **kw),
 }
 
 

@@ -156,3 +156,30 @@ def test_attention_without_a_workspace_on_two_streams_at_once(sru):
     _at_once(sru, *calls)
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_decode_steps_without_a_workspace_on_two_streams_at_once(sru):
+    """(8 rows: the product runs in the workspace that the call allocates)"""
+    d, B = 2048, 8
+    calls, got, want = [], [], []
+    for i in range(2):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        X = torch.randn(B, d, generator=g, device="cuda").bfloat16()
+        W = (torch.randn(3 * d, d, generator=g, device="cuda") * d ** -0.5).bfloat16()
+        x, c0 = X.float(), torch.randn(B, d, generator=g, device="cuda")
+        v, b = torch.randn(2, d, generator=g, device="cuda"), torch.randn(2, d, generator=g, device="cuda")
+        c, h = c0.clone(), torch.empty(B, d, device="cuda")
+
+        def call(stream, X=X, W=W, x=x, v=v, b=b, c=c, h=h):
+            sru.sru_decode_step(X, W, x, v, b, c, h, stream=stream)
+
+        for _ in range(12):  # as often as both streams take it below: the state runs on
+            call(None)
+        torch.cuda.synchronize()
+        want.append([c.clone(), h.clone()])
+        c.copy_(c0)
+        calls.append(call)
+        got.append([c, h])
+    _at_once(sru, *calls)
+    for a, b in zip(sum(got, []), sum(want, [])):
+        assert torch.equal(a, b)
