@@ -2233,7 +2233,7 @@ sru_status sru_sync_status(void* stream) {
         const unsigned zero = 0;
         e = cudaMemcpyToSymbol(sru::g_error_word, &zero, sizeof(zero));
         if (e != cudaSuccess) return cuda_fail(e);
-        return word == sru::kErrBadIndex ? SRU_ERR_INVALID : SRU_ERR_TIMEOUT;
+        return sru::is_timeout(word) ? SRU_ERR_TIMEOUT : SRU_ERR_INVALID;
     }
     return SRU_OK;
 }

@@ -505,7 +505,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         unsigned g0, g1;
                         ld_carry2(cw, g0, g1, c);
                         if (g0 == (unsigned)tt && g1 == (unsigned)tt) break;
-                        if (*reinterpret_cast<volatile unsigned*>(&g_error_word) != 0u) break;
+                        // (a wait that ran out elsewhere leaves nothing to wait for)
+                        if (is_timeout(*reinterpret_cast<volatile unsigned*>(&g_error_word))) break;
                         if (globaltimer_ns() - t0 > kWaitLimitNs) {
                             record_error(kErrTimeoutScan);
                             break;

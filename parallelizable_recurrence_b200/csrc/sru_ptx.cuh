@@ -32,6 +32,10 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
 __device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_error_word, 0u, code); }
 
+// Whether an error word says that a bounded wait ran out.  (An index out of range does not: its
+// kernel skips the entry and nothing is waited for in vain.)
+__host__ __device__ __forceinline__ bool is_timeout(unsigned word) { return word != kErrNone && word != kErrBadIndex; }
+
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

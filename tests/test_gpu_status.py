@@ -1,0 +1,54 @@
+"""What the device error word does to other calls: an index out of range is skipped and reported, and
+changes nothing else.
+"""
+import pytest
+import torch
+
+from test_gpu_fused import _inputs as _fused_inputs
+from test_gpu_loss import _inputs as _loss_inputs
+import sru_testlib as tl
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sru():
+    import parallelizable_recurrence_b200 as m
+    m.load_library()
+    assert m.sru_sync_status() in (m.SRU_OK, m.SRU_ERR_INVALID, m.SRU_ERR_TIMEOUT)  # whatever came before is cleared
+    return m
+
+
+def _bad_target(sru):
+    """A loss with a target behind the vocabulary; nothing reads the status."""
+    H, W, t, _ = _loss_inputs(40, 300, 64, ignored=0.0)
+    t[3] = 300
+    sru.sru_softmax_loss(H, W, t, torch.empty(40, device="cuda"), torch.empty(40, device="cuda"))
+
+
+@pytest.mark.parametrize("L,B,d,nd", [(257, 16, 64, 2), (1024, 16, 512, 1)])
+def test_fused_forward_after_a_bad_target_has_the_same_bits(sru, L, B, d, nd):
+    """The state passes between time tiles on different CTAs: a pending index error must
+    not end the waits for it."""
+    cfg, inp = _fused_inputs(L, B, d, nd, 14, False, True, hole=False)
+    X, W = tl.to_dev_bf16(inp["X"]), tl.to_dev_bf16(inp["W"])
+    x, v, b, c0 = (tl.to_dev_f32(inp[k]) for k in ("x", "v", "bias", "c0"))
+    h = torch.empty(L, B, nd, d, device="cuda")
+    cT = torch.empty(B, nd, d, device="cuda")
+    ws = sru.alloc_workspace(L, B, d, nd == 2)
+
+    def run():
+        h.fill_(float("nan"))
+        cT.fill_(float("nan"))
+        sru.sru_forward_fused(X, W, x, v, b, h, cT, ws, c0=c0, bidirectional=nd == 2)
+
+    run()
+    assert sru.sru_sync_status() == sru.SRU_OK
+    want = h.clone(), cT.clone()
+    assert torch.isfinite(want[0]).all()
+    _bad_target(sru)
+    for _ in range(5):
+        run()
+        assert torch.equal(h, want[0]) and torch.equal(cT, want[1])
+    assert sru.sru_sync_status() == sru.SRU_ERR_INVALID
+    assert sru.sru_sync_status() == sru.SRU_OK
