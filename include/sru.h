@@ -453,7 +453,8 @@ sru_status sru_cache_append(const void* K, int64_t k_ld, const void* V, int64_t 
  *   out[b][i] = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q[b][i] . k_j)
  * over the keys j of head i / (Hq / Hkv) with max(0, lengths[b] - window) <= j <
  * lengths[b] (window = 0: all of them; lengths counts the new token when its row
- * was appended first).  A request without keys gets out = 0 and lse = -inf.
+ * was appended first).  A request without keys, or whose scores are all -inf, gets
+ * out = 0 and lse = -inf; NaN in q or in a key gives NaN in both.
  *   q (B, Hq, D) bf16;  out (B, Hq, D) of type out_t (F32 or BF16), apart from q
  *   lse (B, Hq) fp32, nullable: log sum_j p_j
  * Scores, sums and the result are fp32; p enters the product with v in 16 bits

@@ -140,6 +140,12 @@ struct Cursor {
     }
 };
 
+// log of the sum l of exponentials over their maximum m (base 2), in base e.  Only l = 0, no key that
+// weighs anything, gives -inf: a NaN among scores stays one.
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
 // An item that is in pieces: its place, and its steps in the list.
 struct Item {
     int b, hh, first, last;
@@ -461,8 +467,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                                 s_ml[team][kind][head] = mm;
                                 s_ml[team][kind][8 + head] = ll;
                             } else if (a.lse != nullptr) {
-                                a.lse[(size_t)cur.b * a.Hq + head0 + head] =
-                                    ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : -INFINITY;
+                                a.lse[(size_t)cur.b * a.Hq + head0 + head] = lse_of(mm, ll);
                             }
                         }
                     }
@@ -641,7 +646,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1)
                 *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * a.D + c) =
                     make_uint2(pack_bf16(acc.x * r, acc.y * r), pack_bf16(acc.z * r, acc.w * r));
         }
-        if (a.lse != nullptr && c == 0) a.lse[row] = l > 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (a.lse != nullptr && c == 0) a.lse[row] = lse_of(top, l);
     };
     const size_t pf = piece_floats(tw);
     __syncthreads();
