@@ -478,8 +478,8 @@ sru_status sru_attention_decode(const void* q, const void* k_cache, const void* 
 
 /* Synchronise `stream`, then read and clear the device error word of the
  * current device: SRU_ERR_TIMEOUT if a bounded wait expired since the last
- * call, SRU_ERR_INVALID if a kernel met an index out of range in its data (it
- * skips such an entry), SRU_ERR_CUDA if the stream reported an error, else
+ * call, else SRU_ERR_INVALID if a kernel met an index out of range in its data
+ * (it skips such an entry), SRU_ERR_CUDA if the stream reported an error, else
  * SRU_OK. */
 sru_status sru_sync_status(void* stream);
 

@@ -14,27 +14,29 @@
 
 namespace sru {
 
-// Device error word: first error code recorded on this device since the last
-// sru_sync_status() call (0 = none).  Lives in the library's single
+// Device error word: the largest error code recorded on this device since the
+// last sru_sync_status() call (0 = none).  Lives in the library's single
 // translation unit.
 __device__ unsigned int g_error_word;
 
 enum DeviceError : unsigned {
     kErrNone = 0,
-    kErrTimeoutLoad = 1,      // a TMA load did not land in time
-    kErrTimeoutMma = 2,       // a tensor-core stage did not complete in time
-    kErrTimeoutEpilogue = 3,  // the accumulator was not released in time
-    kErrTimeoutScan = 4,      // a scan predecessor never published its carry
-    kErrBadIndex = 5,         // an index in the call's data (a page, slot or target) is out of range
+    kErrBadIndex = 1,         // an index in the call's data (a page, slot or target) is out of range
+    kErrTimeoutLoad = 2,      // a TMA load did not land in time
+    kErrTimeoutMma = 3,       // a tensor-core stage did not complete in time
+    kErrTimeoutEpilogue = 4,  // the accumulator was not released in time
+    kErrTimeoutScan = 5,      // a scan predecessor never published its carry
 };
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 
-__device__ __forceinline__ void record_error(unsigned code) { atomicCAS(&g_error_word, 0u, code); }
+// (A wait that ran out leaves outputs that cannot be used, a bad index a skipped entry: the
+// former must not hide behind the latter.)
+__device__ __forceinline__ void record_error(unsigned code) { atomicMax(&g_error_word, code); }
 
 // Whether an error word says that a bounded wait ran out.  (An index out of range does not: its
 // kernel skips the entry and nothing is waited for in vain.)
-__host__ __device__ __forceinline__ bool is_timeout(unsigned word) { return word != kErrNone && word != kErrBadIndex; }
+__host__ __device__ __forceinline__ bool is_timeout(unsigned word) { return word > kErrBadIndex; }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -7,6 +7,7 @@ import torch
 from test_gpu_fused import _inputs as _fused_inputs
 from test_gpu_loss import _inputs as _loss_inputs
 import sru_testlib as tl
+from synthetic import SRUConfig, generate
 
 pytestmark = pytest.mark.gpu
 
@@ -50,5 +51,31 @@ def test_fused_forward_after_a_bad_target_has_the_same_bits(sru, L, B, d, nd):
     for _ in range(5):
         run()
         assert torch.equal(h, want[0]) and torch.equal(cT, want[1])
+    assert sru.sru_sync_status() == sru.SRU_ERR_INVALID
+    assert sru.sru_sync_status() == sru.SRU_OK
+
+
+def _withheld_carry(sru):
+    """A scan whose first carry is never published: its bounded waits run out (about 2 s)."""
+    inp = generate(SRUConfig(name="fail", L=256, B=1, d=64, seed=31, proj_dtype="bf16", bias="normal0.1", c0="normal",
+                             v_zero=True), u_direct=True, with_grad=False)
+    L, B, d = inp["x"].shape
+    flags = sru.SRU_FLAG_V_ZERO | sru.SRU_FLAG_FORCE_SCAN
+    sru.sru_forward(tl.dev_U(inp), tl.to_dev_f32(inp["x"]), tl.to_dev_f32(inp["v"]), tl.to_dev_f32(inp["bias"]),
+                    torch.empty(L, B, 1, d, device="cuda"), torch.empty(B, 1, d, device="cuda"),
+                    c0=tl.to_dev_f32(inp["c0"]), workspace=sru.alloc_workspace(L, B, d, False, flags),
+                    flags=flags | sru.SRU_FLAG_TEST_WITHHOLD_CARRY)
+
+
+@pytest.mark.parametrize("order", ["index first", "timeout first"])
+def test_a_wait_that_ran_out_is_reported_beside_a_bad_index(sru, order):
+    """A bad index is skipped, a wait that ran out leaves outputs that cannot be used: of the two the status
+    names the wait."""
+    calls = [_bad_target, _withheld_carry]
+    for call in calls if order == "index first" else calls[::-1]:
+        call(sru)
+    assert sru.sru_sync_status() == sru.SRU_ERR_TIMEOUT
+    assert sru.sru_sync_status() == sru.SRU_OK
+    _bad_target(sru)
     assert sru.sru_sync_status() == sru.SRU_ERR_INVALID
     assert sru.sru_sync_status() == sru.SRU_OK
