@@ -368,7 +368,8 @@ size_t sru_decode_workspace_bytes(int64_t B, int64_t d);
  * A target >= V is reported as SRU_ERR_INVALID by the next sru_sync_status();
  * its row counts like one with a negative target.
  * workspace: >= sru_softmax_loss_workspace_bytes(M, V, K, 0) bytes.
- * Limits: K % 8 == 0; any M >= 0 and V >= 1 below 2^31.  Every pointer is
+ * Limits: K % 8 == 0; any M >= 0 and V >= 1 below 2^31, with fewer than 2^30
+ * squares of 256 x 256 in each of M x V, V x K and M x K.  Every pointer is
  * 16-byte aligned.  fp32 accumulation throughout.
  */
 size_t sru_softmax_loss_workspace_bytes(int64_t M, int64_t V, int64_t K, int backward);

@@ -1755,6 +1755,7 @@ constexpr size_t kLossPieceBytes = (size_t)512 << 20;
 // V32000, loss: 4 / 8 warps 97 / 84 us at K128, 98 / 91 at K256, 112 / 111-114 at K512, 148-151 /
 // 158-164 at K768.
 constexpr int64_t kLossShortK = 384;
+constexpr int64_t kLossMostUnits = (int64_t)1 << 30;  // tiles of a product, and k parts of them: counted in an int
 struct LossPlan {
     int warps;                   // epilogue warps of the vocabulary product
     int64_t parts, Vc, pieces;   // parts of the statistics; piece width and number
@@ -1794,6 +1795,7 @@ static void grad_plan(int64_t M, int64_t n, int64_t K, LossPlan& p) {
                 S[i] = (kb[i] + per - 1) / per;  // no part is empty
                 unit[i] = grad_unit_us(per);
                 units[i] = mt * tn * S[i];
+                if (units[i] >= kLossMostUnits) fits = false;  // (never without a split: check_loss_sizes)
                 if (S[i] > 1) slabs += (double)S[i] * mt * bm * K * 4 * 2 / 5.0e6 + 3.0;
             }
             const double t = grad_us(units[0], unit[0], units[1], unit[1], P) + slabs;
@@ -1832,9 +1834,8 @@ static sru_status check_loss_sizes(int64_t M, int64_t V, int64_t K) {
     if (K % 8 != 0) return SRU_ERR_UNSUPPORTED;
     const int64_t lim = (int64_t)1 << 31;
     if (M >= lim || V >= lim || K >= lim) return SRU_ERR_UNSUPPORTED;
-    if (((M + 255) / 256) * ((V + 255) / 256) >= lim || ((V + 255) / 256) * ((K + 255) / 256) >= lim ||
-        ((M + 255) / 256) * ((K + 255) / 256) >= lim)
-        return SRU_ERR_UNSUPPORTED;
+    const int64_t m = (M + 255) / 256, v = (V + 255) / 256, k = (K + 255) / 256;
+    if (m * v >= kLossMostUnits || v * k >= kLossMostUnits || m * k >= kLossMostUnits) return SRU_ERR_UNSUPPORTED;
     return SRU_OK;
 }
 template <int EPI, int W>
@@ -1991,7 +1992,6 @@ sru_status sru_softmax_loss_backward(const void* H, const void* W, const int64_t
             q.kblocks = (int)kb;
             q.n_tiles = (int)((K + sru::gemm::P_BN - 1) / sru::gemm::P_BN);
             const int64_t units = ((rows[i] + sru::gemm::P_BM - 1) / sru::gemm::P_BM) * q.n_tiles * q.splits;
-            if (units >= (int64_t)1 << 30) return SRU_ERR_UNSUPPORTED;
             q.units = on[i] ? (int)units : 0;
             q.slab_rows = (int)plan[i]->slab_rows;
             q.bf16 = !slabs[i] && type[i] == SRU_BF16;
