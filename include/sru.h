@@ -367,7 +367,8 @@ size_t sru_decode_workspace_bytes(int64_t B, int64_t d);
  *   targets (M) int64;  loss, lse (M) fp32
  * A target >= V is reported as SRU_ERR_INVALID by the next sru_sync_status();
  * its row counts like one with a negative target.
- * workspace: >= sru_softmax_loss_workspace_bytes(M, V, K, 0) bytes.
+ * workspace: >= sru_softmax_loss_workspace_bytes(M, V, K, 0) bytes; calls that may
+ * run at the same time need one each.
  * Limits: K % 8 == 0; any M >= 0 and V >= 1 below 2^31, with fewer than 2^30
  * squares of 256 x 256 in each of M x V, V x K and M x K.  Every pointer is
  * 16-byte aligned.  fp32 accumulation throughout.
@@ -466,7 +467,7 @@ sru_status sru_cache_append(const void* K, int64_t k_ld, const void* V, int64_t 
  * workspace: >= sru_attention_decode_workspace_bytes(B, Hq, Hkv, D) bytes; calls
  * that may run at the same time need one each.  The sums' order depends on the
  * lengths and sizes alone: the same bits every run.
- * Limits: D % 8 == 0, D <= 1024, Hq a multiple of Hkv, B <= 2^20, pages * Hkv,
+ * Limits: D % 8 == 0, D <= 1024, Hq <= 65536 a multiple of Hkv, B <= 2^20, pages * Hkv,
  * pages * page_size and max_pages * page_size below 2^31.  Negative lengths count
  * as 0.  Any page size works; the cache is read in boxes of rows as long as the
  * largest power of two (up to 32) that divides it, so odd sizes are slow.

@@ -1747,9 +1747,10 @@ sru_status sru_decode_step(const void* X_t, const void* W, const float* x_t, con
 }  // extern "C"
 
 // ---- softmax cross entropy over the vocabulary
-// dz of one piece of the vocabulary (M x Vc bf16) stays within this budget.  The
-// gradients read each piece twice; a smaller piece costs one more read and write
-// of the M x K fp32 sum dH, a larger one memory.
+// dz of one piece of the vocabulary (M x Vc bf16) stays within this budget, but a piece has at least
+// four column tiles: above 2^18 rows dz takes 2048 bytes a row (0.6 GB at M300000).  Slabs of split
+// products and the fp32 sum dH (M x K) come on top.  The gradients read each piece twice; a
+// smaller piece costs one more read and write of that sum, a larger one memory.
 constexpr size_t kLossPieceBytes = (size_t)512 << 20;
 // Reduction below which the vocabulary product has eight epilogue warps.  Measured, M4096
 // V32000, loss: 4 / 8 warps 97 / 84 us at K128, 98 / 91 at K256, 112 / 111-114 at K512, 148-151 /
@@ -2151,8 +2152,6 @@ sru_status sru_attention_decode(const void* q, const void* k_cache, const void* 
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     sru::cache::DecodeArgs a{};
     a.q = static_cast<const __nv_bfloat16*>(q);
-    a.k = static_cast<const __nv_bfloat16*>(k_cache);
-    a.v = static_cast<const __nv_bfloat16*>(v_cache);
     a.table = table;
     a.lengths = lengths;
     a.out = out;

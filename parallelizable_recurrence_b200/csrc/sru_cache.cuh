@@ -42,7 +42,7 @@ struct ExtendArgs {
     int rows_kernel;  // long runs of slots are left to cache_slots_kernel
 };
 
-// Inclusive sum over the block's threads; `total` gets the whole sum.
+// Inclusive sum over the warp's lanes.
 __device__ __forceinline__ unsigned long long warp_inclusive(unsigned long long v, int lane) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -51,6 +51,7 @@ __device__ __forceinline__ unsigned long long warp_inclusive(unsigned long long 
     }
     return v;
 }
+// The same over the block's threads; `total` gets the whole sum.
 __device__ __forceinline__ unsigned long long block_inclusive(unsigned long long v, unsigned long long* warp_sums,
                                                               unsigned long long& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;

@@ -49,7 +49,7 @@ constexpr uint32_t kHalfBytes = kStep * 128;        // 64 features of a step's r
 constexpr int kMasks = 8;     // steps whose keys' mask is held
 
 struct DecodeArgs {
-    const __nv_bfloat16 *q, *k, *v;
+    const __nv_bfloat16* q;      // (the caches are read through their maps)
     const int *table, *lengths;
     void* out;
     float* lse;                  // nullable

@@ -17,10 +17,10 @@
 // Four epilogue warps (a thread per row), or eight (two per row) for a short
 // reduction, whose product takes less time than one warp per scheduler needs for a
 // tile's exponentials.
-// The gradients run over pieces of the vocabulary, so that dz never takes more
-// than a bounded buffer; z is recomputed there (2 M V K operations on top of
-// the gradients' 4 M V K): kept, it would take 4 M V bytes (2 GB at M16384 V32000),
-// and writing and reading it as long as the product at K of about 900.
+// The gradients run over pieces of the vocabulary, so that dz takes 512 MB or 2 KB
+// a row at most, whichever is more, and never V columns of them; z is recomputed there (2 M V K
+// operations on top of the gradients' 4 M V K): kept, it would take 4 M V bytes (2 GB at
+// M16384 V32000), and writing and reading it as long as the product at K of about 900.
 // Measured, a kernel alone: M16384 V32000, kStats 702 us at K1024 (1.53 PFLOP/s) and
 // 1.36 ms at K2048 (1.58); M4096 V8192 K1024, kStats 53 us (1.30), both gradient
 // products 98.5 us (1.40).  In a row, long calls settle at the card's power limit.
