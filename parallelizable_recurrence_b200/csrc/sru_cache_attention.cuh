@@ -32,7 +32,8 @@
 // Measured: B96 len <= 8192 D1024 277-301 us (6.0-6.5 TB/s, of 6.56 copied), B24 H32/8
 // D128 len <= 6007 67-72 us, B64 D512 window 2560 57 us (4.7-4.9 TB/s): reading at the
 // memory's rate, plus about 12 us that a call of any size takes (5 to the first loads, 2 to
-// the rate, 4-5 to join) and the spread of the warps' ends.
+// the rate, 4-5 to join) and the spread of the warps' ends.  Of a few keys the kernel takes 11 us
+// (B1 len 200 D512) or 7 (B1 len 37 D64), a chain of latencies.
 #pragma once
 
 #include <type_traits>

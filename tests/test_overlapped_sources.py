@@ -24,7 +24,7 @@ OVERLAPPED = sorted(p for p in glob.glob(os.path.join(CSRC, "*.cuh")) if re.sear
 
 
 def test_the_sources_are_found():
-    assert [os.path.basename(p) for p in OVERLAPPED] == ["sru_cache.cuh", "sru_cache_attention.cuh", "sru_loss.cuh"]
+    assert {"sru_cache.cuh", "sru_cache_attention.cuh", "sru_loss.cuh"} <= {os.path.basename(p) for p in OVERLAPPED}
 
 
 @pytest.mark.parametrize("path", OVERLAPPED, ids=os.path.basename)
