@@ -183,3 +183,45 @@ def test_decode_steps_without_a_workspace_on_two_streams_at_once(sru):
     _at_once(sru, *calls)
     for a, b in zip(sum(got, []), sum(want, [])):
         assert torch.equal(a, b)
+
+
+def test_captured_on_a_forked_stream_without_a_workspace(sru):
+    """A graph whose calls allocate their own workspaces, on the capturing stream and on one forked from
+    it, replayed on new inputs."""
+    M, V, K = 300, 2000, 64
+    H, W, t, w = _inputs(M, V, K)
+    q, kc, vc, table, lengths, _, _ = _decode_inputs(3, 2, 1, 512, [9000, 40, 2000], 16, seed=2)
+    loss, lse, dH = torch.empty(M, device="cuda"), torch.empty(M, device="cuda"), torch.empty(M, K, device="cuda")
+    out, out2 = torch.empty(q.shape, device="cuda"), torch.empty(q.shape, device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        sru.sru_attention_decode(q, kc, vc, table, lengths, out)
+        sru.sru_softmax_loss(H, W, t, loss, lse, stream=side)
+        sru.sru_softmax_loss_backward(H, W, t, lse, w, dH, stream=side)
+        sru.sru_attention_decode(q, kc, vc, table, lengths, out2, stream=side)
+        main.wait_stream(side)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2):
+        H.copy_(_inputs(M, V, K, seed=seed)[0])
+        q.copy_(torch.randn(q.shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda"))
+        step()
+        assert sru.sru_sync_status() == 0
+        torch.cuda.synchronize()
+        want = [x.clone() for x in (loss, lse, dH, out, out2)]
+        assert torch.equal(out, out2)
+        for x in (loss, lse, dH, out, out2):
+            x.fill_(float("nan"))
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert sru.sru_sync_status() == 0
+        for x, y in zip((loss, lse, dH, out, out2), want):
+            assert torch.equal(x, y)
